@@ -272,6 +272,154 @@ ROLA_API rola_status rola_backward(rola_plan_t plan, const void* q, const void* 
  * ROLA_ERR_CUDA if the launch fails. */
 ROLA_API rola_status rola_eval_exp2(const float* x, float* y, int64_t n, int mode, rola_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The operators around RoLA in a video diffusion transformer's block: rotary positions and
+ * norm of q and k before the attention, the gated residual with the next norm after it, and
+ * the dense cross attention to an encoder's states.  They take no plan and keep no state:
+ * every call is described by its parameter struct.  Common rules: device pointers, 16-byte
+ * aligned (positions, kv_len and lse: 4 bytes; key_mask: any); strides in elements, positive
+ * and a multiple of 16 bytes; the strides of an axis of size one are ignored; the last axis
+ * is contiguous.  Errors, streams and the absence of allocations are those of the calls above.  Types: ROLA_F32 and ROLA_BF16 (e4m3: ROLA_ERR_UNSUPPORTED).
+ * Gradients have the type of the tensor they belong to; sums, statistics and the gradients
+ * of parameters are fp32, and every partial sum is reduced in a fixed order.
+ * ------------------------------------------------------------------------------------- */
+
+/* Element strides of a [B, N, H, d] tensor whose channels are contiguous. */
+typedef struct {
+  int64_t b, n, h;
+} rola_strides;
+
+typedef enum {
+  ROLA_NORM_NONE = 0,
+  ROLA_NORM_TOKEN = 1,  /* qk_norm_rope: over a token's H*d channels, weight [H*d]         */
+  ROLA_NORM_HEAD = 2    /* qk_norm_rope: over a head's d channels, weight [d]              */
+} rola_qk_norm;
+
+typedef enum {
+  ROLA_POS_NONE = 0,    /* no rotation (the norm alone)                                    */
+  ROLA_POS_GRID = 1,    /* token n of the grid: (n / (gh*gw), n / gw % gh, n % gw) + start;  */
+                        /* tokens past the grid's gt*gh*gw are not turned                  */
+  ROLA_POS_GIVEN = 2    /* int32 positions [N, 3] or [B, N, 3] (t, h, w), any sign           */
+} rola_pos;
+
+/* qk_norm_rope: for x in {q, k}, per token,
+ *   u = x * w / sqrt(mean(x^2) + eps)   (rola_qk_norm; u = x for ROLA_NORM_NONE)
+ *   y = R(p) u: pair (2c, 2c+1) of every head turned counter-clockwise by
+ *       theta_c = pos_axis(c) * base^(-c'/P_axis), pairs ordered t, h, w as in rola_params
+ * rounded once to the tensor's type.  Angles are formed in fp64 and reduced to one turn
+ * before they are rounded, so far positions keep full accuracy. */
+typedef struct {
+  int B, N, H, d;                /* d 64 | 128, H*d <= 8192                                  */
+  rola_dtype dtype;              /* of q, k and of what is returned                          */
+  rola_dtype grad_dtype;         /* backward: of the upstream gradients (dtype or ROLA_F32)  */
+  rola_qk_norm norm;
+  float eps;                     /* >= 0                                                     */
+  rola_pos pos;
+  int grid_t, grid_h, grid_w;    /* ROLA_POS_GRID: product <= N                               */
+  int start_t, start_h, start_w; /* ROLA_POS_GRID: added to every token's position           */
+  int positions_batched;         /* ROLA_POS_GIVEN: 1 if positions is [B, N, 3]               */
+  int rope_pairs_t, rope_pairs_h, rope_pairs_w; /* sum == d/2; all 0 = default (h = w =       */
+                                 /* floor(d/6), t the rest; a grid with t = h = 1: all on w)  */
+  double rope_base;              /* > 1 (10000)                                              */
+  rola_strides q, k;             /* inputs                                                   */
+  rola_strides dq_out, dk_out;   /* backward: upstream gradients                             */
+} rola_norm_rope_params;
+
+/* B=H=N=1, d=128, bf16, token norm with eps 1e-6, grid (1,1,1), default split, base 10000. */
+ROLA_API rola_status rola_norm_rope_params_default(rola_norm_rope_params* p);
+
+/* q_out, k_out: contiguous [B, N, H, d], or the input itself (in place, its strides).  k,
+ * wk and k_out are null together to treat q alone.  wq, wk: fp32 [H*d] or [d], null for
+ * ROLA_NORM_NONE.  Outputs overlap nothing else. */
+ROLA_API rola_status rola_qk_norm_rope(const rola_norm_rope_params* p, const void* q, const void* k,
+                                       const float* wq, const float* wk, const int32_t* positions,
+                                       void* q_out, void* k_out, rola_stream_t stream);
+
+/* Gradients of sum(dq_out * q_out) + sum(dk_out * k_out): dq, dk contiguous [B, N, H, d] in
+ * p->dtype, dwq, dwk fp32 like wq, wk.  q and k are the forward's inputs (not read, and may
+ * be null, for ROLA_NORM_NONE).  dq may be dq_out itself when types and strides agree.
+ * workspace: rola_qk_norm_rope_workspace_size bytes (0 without a norm), 16-byte aligned. */
+ROLA_API rola_status rola_qk_norm_rope_workspace_size(const rola_norm_rope_params* p, size_t* bytes);
+ROLA_API rola_status rola_qk_norm_rope_backward(const rola_norm_rope_params* p, const void* dq_out,
+                                                const void* dk_out, const void* q, const void* k,
+                                                const float* wq, const float* wk, const int32_t* positions,
+                                                void* dq, void* dk, float* dwq, float* dwk, void* workspace,
+                                                size_t workspace_bytes, rola_stream_t stream);
+
+/* gated_norm: for every token (r is normalised before its rounding to the stored type)
+ *   r = x + gate * branch           (gate absent: 1; branch absent: r = x, not written)
+ *   xhat = (r - mean(r)) / sqrt(var(r) + eps)   or, ROLA_RMS, r / sqrt(mean(r^2) + eps)
+ *   y = xhat * (1 + scale) + shift,  or  xhat * weight + bias,  or xhat
+ * x, r [B, N, C] in x_dtype, branch and y in y_dtype (x_dtype, or ROLA_BF16 beside an fp32
+ * x), all contiguous.  gate, scale, shift: fp32 [B, T, C] with the strides given; token n
+ * takes row n / (N/T) (T = 1: one per sample, T = N: one per token).  weight, bias: fp32
+ * [C].  scale and shift come together, bias only with weight, and one of the two pairs. */
+typedef enum { ROLA_LAYER = 0, ROLA_RMS = 1 } rola_norm_kind;
+
+typedef struct {
+  int B, N, C, T;                /* C a multiple of 8, <= 8192; T divides N                   */
+  rola_dtype x_dtype, y_dtype;
+  rola_norm_kind norm;
+  float eps;                     /* >= 0                                                     */
+  int64_t gate_b, gate_t, scale_b, scale_t, shift_b, shift_t;  /* element strides             */
+} rola_gated_norm_params;
+
+/* x may be r itself; other outputs overlap nothing.  r is null when branch is. */
+ROLA_API rola_status rola_gated_norm(const rola_gated_norm_params* p, const void* x, const void* branch,
+                                     const float* gate, const float* scale, const float* shift,
+                                     const float* weight, const float* bias, void* r, void* y,
+                                     rola_stream_t stream);
+
+/* Gradients of sum(dy * y) + sum(dr * r) at the r that the forward stored (x where it had no
+ * branch): dx [B, N, C] in x_dtype (the gradient of x), dbranch in y_dtype, dgate, dscale,
+ * dshift fp32 [B, T, C] contiguous, dweight, dbias fp32 [C].  dr (x_dtype) may be null: 0.
+ * branch, gate, scale, weight as given to the forward.  dgate is null without gate, dscale
+ * and dshift without scale, dweight without weight; dbias may be null.  dx may be dr. */
+ROLA_API rola_status rola_gated_norm_workspace_size(const rola_gated_norm_params* p, size_t* bytes);
+ROLA_API rola_status rola_gated_norm_backward(const rola_gated_norm_params* p, const void* dy, const void* dr,
+                                              const void* r, const void* branch, const float* gate,
+                                              const float* scale, const float* weight, void* dx, void* dbranch,
+                                              float* dgate, float* dscale, float* dshift, float* dweight,
+                                              float* dbias, void* workspace, size_t workspace_bytes,
+                                              rola_stream_t stream);
+
+/* cross_attend: dense softmax attention of Nq query tokens to the Nk states of an encoder,
+ *   out = softmax(q k^T * scale) v  over the valid keys,  lse = log sum exp(q k^T * scale).
+ * Key m of sample b is valid when m < kv_len[b] (int32 [B], clamped to [0, Nk]; null: Nk) and
+ * key_mask[b, m] != 0 (one byte per key, [B, Nk] contiguous; null: all).  What k and v hold
+ * at invalid keys has no effect, NaN and infinities included, and their gradients are zero;
+ * a sample without a valid key gives out = 0, lse = -inf and zero gradients.
+ * q [B, Nq, H, d], k, v [B, Nk, H, d] with the strides given (d 64 | 128).  out contiguous;
+ * lse [B, H, Nq] fp32, or null in the forward. */
+typedef struct {
+  int B, Nq, Nk, H, d;
+  rola_dtype dtype;
+  float softmax_scale;           /* logit scale; 0 = 1/sqrt(d)                               */
+  rola_strides q, k, v;
+  rola_strides dout;             /* backward: the upstream gradient [B, Nq, H, d]            */
+} rola_cross_params;
+
+/* workspace: rola_cross_workspace_size bytes, 16-byte aligned; 0 bytes where the keys are not
+ * split over blocks (null is then allowed). */
+ROLA_API rola_status rola_cross_workspace_size(const rola_cross_params* p, size_t* bytes);
+ROLA_API rola_status rola_cross_attend(const rola_cross_params* p, const void* q, const void* k, const void* v,
+                                       const int32_t* kv_len, const uint8_t* key_mask, void* out, float* lse,
+                                       void* workspace, size_t workspace_bytes, rola_stream_t stream);
+
+/* Gradients of sum(dout * out): dq [B, Nq, H, d], dk, dv [B, Nk, H, d] contiguous, in p->dtype.
+ * out (contiguous) and lse are the forward's results. */
+ROLA_API rola_status rola_cross_backward_workspace_size(const rola_cross_params* p, size_t* bytes);
+ROLA_API rola_status rola_cross_attend_backward(const rola_cross_params* p, const void* dout, const void* q,
+                                                const void* k, const void* v, const void* out, const float* lse,
+                                                const int32_t* kv_len, const uint8_t* key_mask, void* dq,
+                                                void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                                                rola_stream_t stream);
+
+/* Synchronises `stream`, reads and clears the device status word of the calls above on the
+ * current device (they share it: ROLA_ERR_DEVICE_TIMEOUT if a bounded wait of any of them ran
+ * out since the last poll).  Not during a capture. */
+ROLA_API rola_status rola_block_poll_status(rola_stream_t stream);
+
 ROLA_API const char* rola_status_string(rola_status s);
 
 #ifdef __cplusplus

@@ -1,4 +1,4 @@
-"""RoLA attention forward on NVIDIA B200 (sm_100a): thin Python binding of librola.so.
+"""RoLA attention on NVIDIA B200 (sm_100a): thin Python binding of librola.so.
 
 RoLA ("Rotary-Positioned Low-Rank Linear Attention", the sparse attention module of
 SparkDiffusion) adds a rank-r linear-attention branch with 3D rotary positions to a
@@ -10,6 +10,10 @@ marshals torch tensors (device memory, the current stream) into the C ABI.
 Layouts: q, k, v, out [B, N, H, d]; Wq, Wk [H, d, r]; g [H] fp32 — contiguous, on the
 same CUDA device.  fp32 tensors select the fp32 configuration, bf16 tensors the bf16 one;
 ``dtype="fp8"`` takes bf16 tensors and quantises inside.
+
+The operators that stand around the attention in a transformer block (norm and rotary
+positions of q and k, gated residual with the next norm, cross attention to an encoder's
+states) are in ``block.py``.
 """
 from __future__ import annotations
 
@@ -38,7 +42,11 @@ EXPORTS = ("rola_params_default", "rola_keep_count", "rola_workspace_size", "rol
            "rola_poll_device_status", "rola_set_debug", "rola_status_string",
            "rola_select_blocks_noalloc", "rola_get_fp8_copies", "rola_profile_stages",
            "rola_get_stage_times", "rola_get_attend_redo_count", "rola_eval_exp2",
-           "rola_backward_workspace_size", "rola_backward", "rola_get_block_scores")
+           "rola_backward_workspace_size", "rola_backward", "rola_get_block_scores",
+           "rola_norm_rope_params_default", "rola_qk_norm_rope", "rola_qk_norm_rope_workspace_size",
+           "rola_qk_norm_rope_backward", "rola_gated_norm", "rola_gated_norm_workspace_size",
+           "rola_gated_norm_backward", "rola_cross_workspace_size", "rola_cross_attend",
+           "rola_cross_backward_workspace_size", "rola_cross_attend_backward", "rola_block_poll_status")
 
 
 class RolaError(RuntimeError):
@@ -100,6 +108,18 @@ def load() -> ctypes.CDLL:
         "rola_backward": [P] * 15 + [ctypes.c_size_t, P],
         "rola_get_stage_times": [P, ctypes.POINTER(ctypes.c_float), i32, ctypes.POINTER(i32),
                                  ctypes.POINTER(i32)],
+        "rola_norm_rope_params_default": [P],
+        "rola_qk_norm_rope": [P] * 9,
+        "rola_qk_norm_rope_workspace_size": [P] * 2,
+        "rola_qk_norm_rope_backward": [P] * 13 + [ctypes.c_size_t, P],
+        "rola_gated_norm": [P] * 11,
+        "rola_gated_norm_workspace_size": [P] * 2,
+        "rola_gated_norm_backward": [P] * 16 + [ctypes.c_size_t, P],
+        "rola_cross_workspace_size": [P] * 2,
+        "rola_cross_attend": [P] * 9 + [ctypes.c_size_t, P],
+        "rola_cross_backward_workspace_size": [P] * 2,
+        "rola_cross_attend_backward": [P] * 13 + [ctypes.c_size_t, P],
+        "rola_block_poll_status": [P],
     }.items():
         f = getattr(lib, name)
         f.argtypes = args
@@ -349,5 +369,9 @@ def forward(q, k, v, Wq, Wk, g, topk, grid=None, pairs=(0, 0, 0), rope_base=1000
         plan.close()
 
 
-__all__ = ["Plan", "forward", "select_blocks_noalloc", "load", "make_params", "keep_count", "workspace_size", "RolaError",
+from .block import (block_poll_status, cross_attend, cross_attend_backward, gated_norm,  # noqa: E402
+                    gated_norm_backward, qk_norm_rope, qk_norm_rope_backward)
+
+__all__ = ["Plan", "forward", "qk_norm_rope", "qk_norm_rope_backward", "gated_norm", "gated_norm_backward",
+           "cross_attend", "cross_attend_backward", "block_poll_status", "select_blocks_noalloc", "load", "make_params", "keep_count", "workspace_size", "RolaError",
            "RolaParams", "EXPORTS", "LIB_PATH", "ROLA_DEBUG_STALL_WAIT", "GATES"]
