@@ -196,14 +196,14 @@ CrossArgs args_of(const rola_cross_params& p, const int32_t* kv_len, const uint8
   return a;
 }
 
-// Blocks that share the long axis (`tiles` tiles) of one of `rows` independent tiles: about two
-// blocks for every SM, each with two tiles at least.
-int split_of(long long rows, int tiles) {
-  constexpr long long kWant = 2 * rola::kRowSMs;
-  if (rows * 2 > kWant || tiles < 4) return 1;
-  long long s = kWant / rows;
-  if (s > tiles / 2) s = tiles / 2;
+// Blocks that share the long axis (`tiles` tiles) of one of `rows` independent tiles: `want`
+// blocks in all, each with `least` tiles at least (joining the parts costs a launch and the
+// parts' traffic).
+int split_of(long long rows, int tiles, long long want, int least) {
+  long long s = want / rows;
+  if (s > tiles / least) s = tiles / least;
   if (s > 64) s = 64;
+  if (s < 2) return 1;
   const int run = (int)((tiles + s - 1) / s);
   return (tiles + run - 1) / run;
 }
@@ -211,22 +211,29 @@ int split_of(long long rows, int tiles) {
 struct CrossSplits {
   int keys, queries;
 };
-CrossSplits splits_of(const rola_cross_params& p) {
-  constexpr int kTile = 64;
-  const int tq = (p.Nq + kTile - 1) / kTile, tk = (p.Nk + kTile - 1) / kTile;
+int tiles_of(int n, int tile) { return (n - 1) / tile + 1; }
+// Forward: blocks that share a query tile's keys (fp32: tiles of 64 x 64, two blocks an SM;
+// bf16: of 256 queries x 128 keys, one).
+int forward_splits(const rola_cross_params& p) {
   const long long bh = (long long)p.B * p.H;
-  return {split_of(bh * tq, tk), split_of(bh * tk, tq)};
+  if (p.dtype == ROLA_F32) return split_of(bh * tiles_of(p.Nq, 64), tiles_of(p.Nk, 64), 2 * rola::kRowSMs, 2);
+  return split_of(bh * tiles_of(p.Nq, 256), tiles_of(p.Nk, 128), rola::kRowSMs, 4);
+}
+CrossSplits backward_splits(const rola_cross_params& p) {
+  const int tq = tiles_of(p.Nq, 64), tk = tiles_of(p.Nk, 64);
+  const long long bh = (long long)p.B * p.H;
+  return {split_of(bh * tq, tk, 2 * rola::kRowSMs, 2), split_of(bh * tk, tq, 2 * rola::kRowSMs, 2)};
 }
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 size_t forward_bytes(const rola_cross_params& p) {
-  const CrossSplits s = splits_of(p);
-  return s.keys == 1 ? 0 : 4 * (size_t)s.keys * p.B * p.Nq * p.H * (p.d + 1);
+  const int s = forward_splits(p);
+  return s == 1 ? 0 : 4 * (size_t)s * p.B * p.Nq * p.H * (p.d + 1);
 }
 
 size_t backward_bytes(const rola_cross_params& p) {
-  const CrossSplits s = splits_of(p);
+  const CrossSplits s = backward_splits(p);
   const size_t q = s.keys == 1 ? 0 : 4 * (size_t)s.keys * p.B * p.Nq * p.H * p.d;
   const size_t k = s.queries == 1 ? 0 : 8 * (size_t)s.queries * p.B * p.Nk * p.H * p.d;
   return align16(4 * (size_t)p.B * p.H * p.Nq) + (q > k ? q : k);
@@ -453,9 +460,13 @@ rola_status rola_cross_attend(const rola_cross_params* p, const void* q, const v
     if (kv_len && overlaps(outs[a].p, outs[a].n, kv_len, 4 * (size_t)p->B)) return ROLA_ERR_INVALID_ARG;
     if (key_mask && overlaps(outs[a].p, outs[a].n, key_mask, (size_t)p->B * p->Nk)) return ROLA_ERR_INVALID_ARG;
   }
-  return cuda_status(rola::launch_cross_simt(args_of(*p, kv_len, key_mask), p->dtype, splits_of(*p).keys, q, k, v, out,
-                                             lse, static_cast<float*>(workspace),
-                                             reinterpret_cast<cudaStream_t>(stream)));
+  const CrossArgs a = args_of(*p, kv_len, key_mask);
+  const int splits = forward_splits(*p);
+  float* part = static_cast<float*>(workspace);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (p->dtype == ROLA_F32)
+    return cuda_status(rola::launch_cross_simt(a, p->dtype, splits, q, k, v, out, lse, part, st));
+  return cuda_status(rola::launch_cross_sm100(a, splits, q, k, v, out, lse, part, st));
 }
 
 rola_status rola_cross_backward_workspace_size(const rola_cross_params* p, size_t* bytes) {
@@ -495,7 +506,7 @@ rola_status rola_cross_attend_backward(const rola_cross_params* p, const void* d
     if (kv_len && overlaps(outs[a].p, outs[a].n, kv_len, 4 * (size_t)p->B)) return ROLA_ERR_INVALID_ARG;
     if (key_mask && overlaps(outs[a].p, outs[a].n, key_mask, (size_t)p->B * p->Nk)) return ROLA_ERR_INVALID_ARG;
   }
-  const CrossSplits sp = splits_of(*p);
+  const CrossSplits sp = backward_splits(*p);
   float* drow = static_cast<float*>(workspace);
   float* part = drow + align16(4 * rows) / 4;
   return cuda_status(rola::launch_cross_simt_backward(args_of(*p, kv_len, key_mask), p->dtype, sp.queries, sp.keys,
@@ -504,7 +515,11 @@ rola_status rola_cross_attend_backward(const rola_cross_params* p, const void* d
 }
 
 rola_status rola_block_poll_status(rola_stream_t stream) {
-  return cuda_status(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int word = 0;
+  if (cudaStreamSynchronize(st) != cudaSuccess || rola::cross_sm100_status(&word, st) != cudaSuccess)
+    return ROLA_ERR_CUDA;
+  return static_cast<rola_status>(word);
 }
 
 }  // extern "C"

@@ -58,6 +58,14 @@ struct CrossArgs {
   const uint8_t* key_mask;
 };
 
+bool make_heads_map(CUtensorMap* m, const void* ptr, int B, int N, int H, int d, const rola_strides& s,
+                    uint32_t rows);
+// The bf16 forward on the tensor cores; `splits` blocks share a query tile's keys as below.
+cudaError_t launch_cross_sm100(const CrossArgs& a, int splits, const void* q, const void* k, const void* v, void* out,
+                               float* lse, float* part, cudaStream_t st);
+// Reads and clears this device's status word of those kernels.
+cudaError_t cross_sm100_status(int* word, cudaStream_t st);
+
 // Joins `splits` parts of the forward (each with its own softmax: [splits][B, Nq, H, d] fp32 and
 // [splits][B, H, Nq]); sums `parts` parts of a gradient, `stride` floats apart.
 cudaError_t launch_cross_join(const CrossArgs& a, rola_dtype dt, int splits, const float* part, const float* plse,

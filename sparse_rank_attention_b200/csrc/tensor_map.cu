@@ -52,4 +52,20 @@ bool make_map_3d(CUtensorMap* m, CUtensorMapDataType dt, uint32_t el_bytes, cons
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A strided [B, N, H, d] bf16 tensor as a 4D map (channels, heads, tokens, batch) with boxes of
+// `rows` tokens of one head x 64 channels, 128-byte swizzle; tokens past N read as zeros and are
+// clipped on stores.
+bool make_heads_map(CUtensorMap* m, const void* ptr, int B, int N, int H, int d, const rola_strides& s,
+                    uint32_t rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)N, (cuuint64_t)B};
+  cuuint64_t strides[3] = {(cuuint64_t)s.h * 2, (cuuint64_t)s.n * 2, (cuuint64_t)s.b * 2};
+  cuuint32_t box[4] = {64, 1, rows, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace rola
