@@ -219,10 +219,15 @@ int forward_splits(const rola_cross_params& p) {
   if (p.dtype == ROLA_F32) return split_of(bh * tiles_of(p.Nq, 64), tiles_of(p.Nk, 64), 2 * rola::kRowSMs, 2);
   return split_of(bh * tiles_of(p.Nq, 256), tiles_of(p.Nk, 128), rola::kRowSMs, 4);
 }
+// Backward: the same for dq, and blocks that share a key tile's queries for dk, dv (bf16: tiles
+// of 128 keys x 128 queries; several items per SM even out the last round of blocks).
 CrossSplits backward_splits(const rola_cross_params& p) {
-  const int tq = tiles_of(p.Nq, 64), tk = tiles_of(p.Nk, 64);
   const long long bh = (long long)p.B * p.H;
-  return {split_of(bh * tq, tk, 2 * rola::kRowSMs, 2), split_of(bh * tk, tq, 2 * rola::kRowSMs, 2)};
+  if (p.dtype == ROLA_F32) {
+    const int tq = tiles_of(p.Nq, 64), tk = tiles_of(p.Nk, 64);
+    return {split_of(bh * tq, tk, 2 * rola::kRowSMs, 2), split_of(bh * tk, tq, 2 * rola::kRowSMs, 2)};
+  }
+  return {forward_splits(p), split_of(bh * tiles_of(p.Nk, 128), tiles_of(p.Nq, 128), 8 * rola::kRowSMs, 8)};
 }
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
@@ -232,11 +237,17 @@ size_t forward_bytes(const rola_cross_params& p) {
   return s == 1 ? 0 : 4 * (size_t)s * p.B * p.Nq * p.H * (p.d + 1);
 }
 
+// Statistics per row: D (fp32), or lse and D in padded rows (bf16).
+size_t stats_bytes(const rola_cross_params& p) {
+  if (p.dtype == ROLA_F32) return align16(4 * (size_t)p.B * p.H * p.Nq);
+  return 8 * (size_t)p.B * p.H * rola::cross_padded_rows(p.Nq);
+}
+
 size_t backward_bytes(const rola_cross_params& p) {
   const CrossSplits s = backward_splits(p);
   const size_t q = s.keys == 1 ? 0 : 4 * (size_t)s.keys * p.B * p.Nq * p.H * p.d;
   const size_t k = s.queries == 1 ? 0 : 8 * (size_t)s.queries * p.B * p.Nk * p.H * p.d;
-  return align16(4 * (size_t)p.B * p.H * p.Nq) + (q > k ? q : k);
+  return stats_bytes(p) + (q > k ? q : k);
 }
 
 }  // namespace
@@ -507,19 +518,25 @@ rola_status rola_cross_attend_backward(const rola_cross_params* p, const void* d
     if (key_mask && overlaps(outs[a].p, outs[a].n, key_mask, (size_t)p->B * p->Nk)) return ROLA_ERR_INVALID_ARG;
   }
   const CrossSplits sp = backward_splits(*p);
-  float* drow = static_cast<float*>(workspace);
-  float* part = drow + align16(4 * rows) / 4;
-  return cuda_status(rola::launch_cross_simt_backward(args_of(*p, kv_len, key_mask), p->dtype, sp.queries, sp.keys,
-                                                      dout, q, k, v, out, lse, dq, dk, dv, drow, part,
-                                                      reinterpret_cast<cudaStream_t>(stream)));
+  float* stats = static_cast<float*>(workspace);
+  float* part = stats + stats_bytes(*p) / 4;
+  const CrossArgs a = args_of(*p, kv_len, key_mask);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (p->dtype == ROLA_F32)
+    return cuda_status(rola::launch_cross_simt_backward(a, p->dtype, sp.queries, sp.keys, dout, q, k, v, out, lse, dq,
+                                                        dk, dv, stats, part, st));
+  return cuda_status(rola::launch_cross_sm100_backward(a, sp.queries, sp.keys, dout, q, k, v, out, lse, dq, dk, dv,
+                                                       stats, part, st));
 }
 
 rola_status rola_block_poll_status(rola_stream_t stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int word = 0;
-  if (cudaStreamSynchronize(st) != cudaSuccess || rola::cross_sm100_status(&word, st) != cudaSuccess)
+  int back = 0;
+  if (cudaStreamSynchronize(st) != cudaSuccess || rola::cross_sm100_status(&word, st) != cudaSuccess ||
+      rola::cross_sm100_backward_status(&back, st) != cudaSuccess)
     return ROLA_ERR_CUDA;
-  return static_cast<rola_status>(word);
+  return static_cast<rola_status>(word ? word : back);
 }
 
 }  // extern "C"

@@ -63,8 +63,17 @@ bool make_heads_map(CUtensorMap* m, const void* ptr, int B, int N, int H, int d,
 // The bf16 forward on the tensor cores; `splits` blocks share a query tile's keys as below.
 cudaError_t launch_cross_sm100(const CrossArgs& a, int splits, const void* q, const void* k, const void* v, void* out,
                                float* lse, float* part, cudaStream_t st);
-// Reads and clears this device's status word of those kernels.
+// Its gradients: rows of softmax statistics first, then dq, then dk and dv.  stats: 2 * B * H *
+// cross_padded_rows(Nq) floats.  splits_k as in the forward; splits_q blocks share a key tile's
+// queries.
+inline size_t cross_padded_rows(int Nq) { return ((size_t)Nq + 255) / 256 * 256; }
+cudaError_t launch_cross_sm100_backward(const CrossArgs& a, int splits_q, int splits_k, const void* dout,
+                                        const void* q, const void* k, const void* v, const void* out,
+                                        const float* lse, void* dq, void* dk, void* dv, float* stats, float* part,
+                                        cudaStream_t st);
+// Read and clear this device's status word of those kernels.
 cudaError_t cross_sm100_status(int* word, cudaStream_t st);
+cudaError_t cross_sm100_backward_status(int* word, cudaStream_t st);
 
 // Joins `splits` parts of the forward (each with its own softmax: [splits][B, Nq, H, d] fp32 and
 // [splits][B, H, Nq]); sums `parts` parts of a gradient, `stride` floats apart.

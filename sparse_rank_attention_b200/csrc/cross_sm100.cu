@@ -25,9 +25,7 @@
 #include <climits>
 #include <cuda.h>
 
-#include "block_internal.cuh"
-#include "sm100_ptx.cuh"
-#include "softmax_exp.cuh"
+#include "cross_sm100.cuh"
 
 namespace rola {
 namespace {
@@ -37,8 +35,6 @@ using namespace sm100;
 __device__ int g_status[1];
 
 constexpr int kThreads = 384;
-constexpr int kTile = 128;                    // queries of a tile, keys of a tile
-constexpr uint32_t kBox = 128 * 128;          // bytes of a box: 128 rows x 64 channels
 constexpr float kSlack = 8.f;                 // log2 units a score may exceed its row's offset by
 
 template <int D>
@@ -63,57 +59,6 @@ struct Ctl {
 
 template <int D>
 constexpr size_t smem_bytes() { return Geo<D>::kOffCtl + sizeof(Ctl) + 1024; }
-
-// One work item: a pair of query tiles of one head over a run of key tiles.
-struct Item {
-  int b, h, q0, streams, t0, t1, split;
-};
-struct Work {
-  int pairs, splits, run, items;
-};
-__device__ __forceinline__ int key_count(const CrossArgs& a, int b) {
-  return a.kv_len ? min(max(__ldg(a.kv_len + b), 0), a.Nk) : a.Nk;
-}
-__device__ __forceinline__ Item item_at(const CrossArgs& a, const Work& w, int i) {
-  Item x;
-  const int bh = i / (w.pairs * w.splits), rest = i - bh * w.pairs * w.splits;
-  const int pair = rest / w.splits;
-  x.split = rest - pair * w.splits;
-  x.b = bh / a.H;
-  x.h = bh - x.b * a.H;
-  x.q0 = pair * 2 * kTile;
-  x.streams = x.q0 + kTile < a.Nq ? 2 : 1;
-  x.t0 = x.split * w.run;
-  x.t1 = max(x.t0, min((key_count(a, x.b) + kTile - 1) / kTile, x.t0 + w.run));
-  return x;
-}
-// The next item at or after i that has key tiles (all others need no products), or one past the end.
-__device__ __forceinline__ int next_item(const CrossArgs& a, const Work& w, int i, Item* x) {
-  for (; i < w.items; i += gridDim.x) {
-    *x = item_at(a, w, i);
-    if (x->t1 > x->t0) return i;
-  }
-  return w.items;
-}
-
-// The 128 validity bits of key tile t (warp-collective): word e holds keys 32e .. 32e + 31.
-__device__ __forceinline__ void tile_bits(const CrossArgs& a, int b, int len, int t, int lane, uint32_t (&bits)[4]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int m = t * kTile + 32 * e + lane;
-    bool ok = m < len;
-    if (a.key_mask && ok) ok = __ldg(a.key_mask + (size_t)b * a.Nk + m) != 0;
-    bits[e] = __ballot_sync(0xffffffffu, ok);
-  }
-}
-__device__ __forceinline__ bool all_set(const uint32_t (&bits)[4]) {
-  return (bits[0] & bits[1] & bits[2] & bits[3]) == 0xffffffffu;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
@@ -283,14 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
         ok = __all_sync(0xffffffffu, mbar_wait(bar(ctl->kv_full[s]), (n / kStages) & 1, wc));
         if (!ok) break;
         if (!all_set(bits)) {
-          uint8_t* tile = base + G::kOffKV + s * G::kTileBytes;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!((bits[e] >> lane) & 1u))
-              for (int c = 0; c < G::kBoxes; ++c)
-#pragma unroll
-                for (int o = 0; o < 8; ++o)
-                  *reinterpret_cast<uint4*>(tile + c * kBox + (32 * e + lane) * 128 + 16 * o) = make_uint4(0, 0, 0, 0);
+          clear_rows<G::kBoxes>(base + G::kOffKV + s * G::kTileBytes, bits, lane);
           fence_proxy_async_smem();
         }
         __syncwarp();
@@ -473,6 +411,7 @@ cudaError_t launch(const CrossArgs& a, int splits, const void* q, const void* k,
   const long long items = (long long)a.B * a.H * w.pairs * splits;
   if (items > INT_MAX - 4096) return cudaErrorInvalidValue;
   w.items = (int)items;
+  w.padded = 0;
   float* plse = part + (size_t)splits * a.B * a.Nq * a.H * D;
   const unsigned long long limit_cycles = 2000000000ull;   // 1 s at 2 GHz
   cross_sm100_kernel<D><<<(unsigned)(items < sms ? items : sms), kThreads, smem, st>>>(tq, tk, tv, to, a, w, lse, part,
@@ -490,13 +429,6 @@ cudaError_t launch_cross_sm100(const CrossArgs& a, int splits, const void* q, co
                    : launch<128>(a, splits, q, k, v, out, lse, part, st);
 }
 
-cudaError_t cross_sm100_status(int* word, cudaStream_t st) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  if (e != cudaSuccess || *word == 0) return e;
-  static const int zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
-  return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
-}
+cudaError_t cross_sm100_status(int* word, cudaStream_t st) { return take_status(g_status, word, st); }
 
 }  // namespace rola
