@@ -85,7 +85,7 @@ rola_status check(const rola_norm_rope_params* p) {
   if (p->grad_dtype != p->dtype && p->grad_dtype != ROLA_F32) return ROLA_ERR_UNSUPPORTED;
   if (p->d != 64 && p->d != 128) return ROLA_ERR_UNSUPPORTED;
   if ((long long)p->H * p->d > rola::kMaxRowChannels) return ROLA_ERR_UNSUPPORTED;
-  if ((long long)p->B * p->N > kMaxRows) return ROLA_ERR_UNSUPPORTED;
+  if ((long long)p->B * p->N > kMaxRows || p->B > kMaxGrid) return ROLA_ERR_UNSUPPORTED;
   if (p->pos == ROLA_POS_NONE) return ROLA_OK;
   if (!(p->rope_base > 1.0) || std::isinf(p->rope_base)) return ROLA_ERR_INVALID_ARG;
   if (p->rope_pairs_t < 0 || p->rope_pairs_h < 0 || p->rope_pairs_w < 0) return ROLA_ERR_INVALID_ARG;
@@ -308,7 +308,12 @@ rola_status rola_qk_norm_rope_workspace_size(const rola_norm_rope_params* p, siz
   const rola_status s = check(p);
   if (s != ROLA_OK) return s;
   const int C = p->H * p->d;
-  *bytes = p->norm == ROLA_NORM_NONE ? 0 : 8 * (size_t)C * rola::norm_rope_parts((long long)p->B * p->N, C);
+  if (p->norm == ROLA_NORM_NONE) {
+    *bytes = 0;
+    return ROLA_OK;
+  }
+  const int one = rola::norm_rope_parts(p->B, p->N, C, 1), two = rola::norm_rope_parts(p->B, p->N, C, 2);
+  *bytes = 8 * (size_t)C * (one > two ? one : two);
   return ROLA_OK;
 }
 

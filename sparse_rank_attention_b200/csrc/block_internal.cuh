@@ -22,8 +22,8 @@ struct NormRopeArgs {
   RotArgs rot;
 };
 
-// Partial rows of dw that a launch over `rows` rows of C channels may write.
-int norm_rope_parts(long long rows, int C);
+// Partial rows of dw that a launch over rows of C channels of one or two tensors writes.
+int norm_rope_parts(int B, int N, int C, int tensors);
 cudaError_t launch_norm_rope(const NormRopeArgs& a, rola_dtype dt, rola_qk_norm norm, const void* q, const void* k,
                              const float* wq, const float* wk, void* qo, void* ko, cudaStream_t st);
 cudaError_t launch_norm_rope_backward(const NormRopeArgs& a, rola_dtype dt, rola_dtype gdt, rola_qk_norm norm,

@@ -6,282 +6,469 @@
 //   dbranch = gate * dx;  dgate = sum dx * branch;  dA = sum dy * xhat;  dB = sum dy,
 //   the sums over the tokens that share a row of the modulation (all tokens for weight, bias).
 //
-// Bound by memory: each tensor is read or written once.  A group of warps owns a token, a
-// thread the same 8 channels of every token it meets, so that the modulation stays in registers
-// while the tokens share it and the column sums of the backward are private to a thread.  The
-// variance is taken about the mean of the values held in registers (a second sum, not
-// E[x^2] - E[x]^2, which loses everything when the mean is large).
+// Bound by memory: each tensor is read or written once.  A group of warps owns a token; a thread
+// has the same vectors of 8 channels of every token it meets, so that the modulation stays in
+// registers while the tokens share it and the column sums of the backward are private to a
+// thread.  The variance is taken about the mean of the values held in registers (a second sum,
+// not E[x^2] - E[x]^2, which loses everything when the mean is large).
+#include <type_traits>
+
 #include "block_internal.cuh"
 #include "row_ops.cuh"
 
 namespace rola {
 namespace {
 
-constexpr int kThreadsPerSM = 1536;   // resident threads that the forward's grid is sized for
-constexpr int kGroupsMost = 8;
-constexpr int kRed = kMaxRowWarps * 2 + kGroupsMost * 2;
+constexpr int kThreadsPerSM = 1024;   // resident threads that a grid is sized for
+constexpr size_t kRing = 192 * 1024;  // shared memory for the rows in flight of a block
+constexpr int kMaxGroups = 4;
+constexpr int kMaxV = 2;              // vectors of a thread
+constexpr int kMaxThreads = 512;      // 8192 channels
+constexpr int kMaxWarps = kMaxThreads / 32;
 
-__device__ __forceinline__ void load8f(const float* p, float* v) {
-  Raw8<float> r;
-  r.load(p);
-  r.get(v);
-}
+struct Shared {
+  alignas(16) float red[2][kMaxGroups][2 * kMaxWarps];
+};
 
-template <typename TX, typename TY, bool LAYER>
-__global__ void __launch_bounds__(1024) gated_norm_kernel(const __grid_constant__ GatedNormArgs a, int W,
-                                                          const TX* x, const TY* __restrict__ branch,
-                                                          const float* __restrict__ gate,
-                                                          const float* __restrict__ scale,
-                                                          const float* __restrict__ shift,
-                                                          const float* __restrict__ weight,
-                                                          const float* __restrict__ bias, TX* r, TY* __restrict__ y) {
-  __shared__ float red[2][kRed];
-  const RowGroup rg(W);
-  const int G = blockDim.x / (32 * W);
-  const int c = kVec * rg.t;
-  const bool on = c < a.C;
-  const long long rows = (long long)a.B * a.N, step = (long long)gridDim.x * G;
-  const float inv = 1.f / a.C;
-  float mg[kVec], ma[kVec], mb[kVec];
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    mg[i] = 1.f;
-    ma[i] = weight && on ? __ldg(weight + c + i) : 1.f;
-    mb[i] = bias && on ? __ldg(bias + c + i) : 0.f;
+RowShape shape_of(int C) { return row_shape(C, kMaxV, kMaxWarps); }
+
+// A group's walk over its rows: the tokens of segment `seg`, then of seg + groups, ...; a segment
+// is a chunk of the tokens that share a modulation row.
+struct Cursor {
+  long long seg;
+  int b, t, n, n1;
+  __device__ __forceinline__ void open(const GatedNormArgs& a, long long segs) {
+    if (seg >= segs) return;
+    const unsigned mod = (unsigned)(seg / a.chunks), ch = (unsigned)(seg - (long long)mod * a.chunks);
+    b = mod / (unsigned)a.T;
+    t = mod - b * a.T;
+    n = t * a.per + ch * a.chunk;
+    n1 = min(n + a.chunk, (t + 1) * a.per);
   }
-  long long held = -1;                 // the modulation row in registers
-  Raw8<TX> nx;
-  Raw8<TY> nb;
-  nx.zero();
-  nb.zero();
-  auto fetch = [&](long long row) {
-    if (row < rows && on) {
-      nx.load(x + row * a.C + c);
-      if (branch) nb.load(branch + row * a.C + c);
-    }
-  };
-  long long row = (long long)blockIdx.x * G + rg.g;
-  fetch(row);
-  for (; row < rows; row += step) {
-    const int b = (int)(row / a.N), n = (int)(row - (long long)b * a.N), t = n / a.per;
-    const long long mod = (long long)b * a.T + t;
-    if (mod != held && on) {
-      held = mod;
-      if (gate) load8f(gate + b * a.gate_b + t * a.gate_t + c, mg);
-      if (scale) {
-        load8f(scale + b * a.scale_b + t * a.scale_t + c, ma);
-        load8f(shift + b * a.shift_b + t * a.shift_t + c, mb);
+  // the next row; true where it opens a segment
+  __device__ __forceinline__ bool next(const GatedNormArgs& a, long long segs, long long groups) {
+    if (++n < n1) return false;
+    seg += groups;
+    open(a, segs);
+    return true;
+  }
+};
+
+template <typename TX, typename TY, bool LAYER, bool BRANCH, int V, int kAhead>
+__global__ void __launch_bounds__(kMaxThreads) gated_norm_kernel(
+    const __grid_constant__ GatedNormArgs a, int W, const TX* x, const TY* __restrict__ branch,
+    const float* __restrict__ gate, const float* __restrict__ scale, const float* __restrict__ shift,
+    const float* __restrict__ weight, const float* __restrict__ bias, TX* r, TY* __restrict__ y) {
+  constexpr int kPx = Raw8<TX>::kPieces, kPb = BRANCH ? Raw8<TY>::kPieces : 0, kPieces = V * (kPx + kPb);
+  __shared__ Shared sh;
+  extern __shared__ uint4 ring[];      // [kAhead][pieces][threads]
+  const RowGroup rg(W);
+  const int G = blockDim.x / (32 * W), nt = blockDim.x, c0 = kVec * rg.t, cs = kVec * 32 * W;
+  const float inv = 1.f / a.C;
+  const long long segs = (long long)a.B * a.T * a.chunks, groups = (long long)gridDim.x * G;
+  float mg[V][kVec], ma[V][kVec], mb[V][kVec];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) ma[i] += 1.f;
+  for (int j = 0; j < V; ++j)
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int c = c0 + j * cs + i;
+      mg[j][i] = 1.f;
+      ma[j][i] = weight && c < a.C ? __ldg(weight + c) : 1.f;
+      mb[j][i] = bias && c < a.C ? __ldg(bias + c) : 0.f;
+    }
+  uint4* mine = ring + threadIdx.x;
+  Cursor ahead{(long long)blockIdx.x * G + rg.g, 0, 0, 0, 0};
+  ahead.open(a, segs);
+  Cursor now = ahead;
+  auto fetch = [&](int s) {
+    if (ahead.seg < segs) {
+      const size_t row = (size_t)ahead.b * a.N + ahead.n;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = c0 + j * cs;
+        if (c < a.C) {
+          uint4* at = mine + (s * kPieces + j * (kPx + kPb)) * nt;
+          copy_vec(at, nt, x + row * a.C + c);
+          if (BRANCH) copy_vec(at + kPx * nt, nt, branch + row * a.C + c);
+        }
+      }
+      ahead.next(a, segs, groups);
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead - 1; ++s) fetch(s);
+  bool open = true;
+  for (int it = 0, slot = 0; now.seg < segs; ++it) {
+    {
+      const size_t row = (size_t)now.b * a.N + now.n;
+      if (open) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int c = c0 + j * cs;
+          if (c < a.C) {
+            if (gate) load8(gate + now.b * a.gate_b + now.t * a.gate_t + c, mg[j]);
+            if (scale) {
+              load8(scale + now.b * a.scale_b + now.t * a.scale_t + c, ma[j]);
+              load8(shift + now.b * a.shift_b + now.t * a.shift_t + c, mb[j]);
+#pragma unroll
+              for (int i = 0; i < kVec; ++i) ma[j][i] += 1.f;
+            }
+          }
+        }
+      }
+      fetch(slot == 0 ? kAhead - 1 : slot - 1);
+      copy_wait<kAhead - 1>();
+      float v[V][kVec];
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = c0 + j * cs;
+        const uint4* at = mine + (slot * kPieces + j * (kPx + kPb)) * nt;
+        if (c < a.C) {
+          Raw8<TX> rx;
+          rx.slot(at, nt);
+          rx.get(v[j]);
+          if (BRANCH) {
+            Raw8<TY> rb;
+            float u[kVec];
+            rb.slot(at + kPx * nt, nt);
+            rb.get(u);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[j][i] = fmaf(mg[j][i], u[i], v[j][i]);
+            store8(r + row * a.C + c, v[j]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) v[j][i] = 0.f;
+        }
+        if (LAYER) {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) sum += v[j][i];
+        }
+      }
+      if (LAYER) {
+        const float mean = group_sum(rg, sum, sh.red[0][rg.g]) * inv;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) v[j][i] = c0 + j * cs < a.C ? v[j][i] - mean : 0.f;
+      }
+      float sq = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sq = fmaf(v[j][i], v[j][i], sq);
+      const float rstd = rsqrtf(fmaf(group_sum(rg, sq, sh.red[LAYER ? 1 : it & 1][rg.g]), inv, a.eps));
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = c0 + j * cs;
+        if (c < a.C) {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) v[j][i] = fmaf(v[j][i] * rstd, ma[j][i], mb[j][i]);
+          store8(y + row * a.C + c, v[j]);
+        }
       }
     }
-    float v[kVec], u[kVec];
-    nx.get(v);
-    nb.get(u);
-    fetch(row + step);
-    if (branch) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = fmaf(mg[i], u[i], v[i]);
-      if (on) store8(r + row * a.C + c, v);
-    }
-    if (LAYER) {
-      float s[1] = {0.f};
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) s[0] += v[i];
-      group_sum<1>(rg, s, red[0] + rg.g * (W + 1));
-      const float mean = s[0] * inv;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = on ? v[i] - mean : 0.f;
-    }
-    float s[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) s[0] = fmaf(v[i], v[i], s[0]);
-    group_sum<1>(rg, s, red[1] + rg.g * (W + 1));
-    if (!LAYER) rg.sync();             // red[1] is written again by the next row
-    const float rstd = rsqrtf(fmaf(s[0], inv, a.eps));
-    if (on) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = fmaf(v[i] * rstd, ma[i], mb[i]);
-      store8(y + row * a.C + c, v);
-    }
+    slot = slot == kAhead - 1 ? 0 : slot + 1;
+    open = now.next(a, segs, groups);
   }
+  copy_wait<0>();
 }
 
 // A group takes one segment after the other: a chunk of the tokens that share a modulation
 // row.  A segment's column sums go to msum, [segments][3][C] (dgate, dscale, dshift): the
 // gradients themselves where a modulation row is one segment (outputs given), else partial
 // sums.  The sums of weight and bias run over all segments of the group: wsum [groups][2][C].
-template <typename TX, typename TY, bool LAYER>
-__global__ void __launch_bounds__(1024) gated_norm_backward_kernel(
+template <typename TX, typename TY, bool LAYER, bool DR, bool BRANCH, int V, int kAhead>
+__global__ void __launch_bounds__(kMaxThreads) gated_norm_backward_kernel(
     const __grid_constant__ GatedNormArgs a, int W, const TY* __restrict__ dy, const TX* dr,
     const TX* __restrict__ r, const TY* __restrict__ branch, const float* __restrict__ gate,
     const float* __restrict__ scale, const float* __restrict__ weight, TX* dx, TY* __restrict__ dbranch,
     float* __restrict__ dgate, float* __restrict__ dscale, float* __restrict__ dshift, int64_t sum_stride,
     float* __restrict__ wsum) {
-  __shared__ float red[2][kRed];
+  constexpr int kPx = Raw8<TX>::kPieces, kPy = Raw8<TY>::kPieces;
+  constexpr int kD = kPx + kPy, kB = kD + (DR ? kPx : 0), kEach = kB + (BRANCH ? kPy : 0), kPieces = V * kEach;
+  __shared__ Shared sh;
+  extern __shared__ uint4 ring[];      // [kAhead][pieces][threads]: r, dy, dr, branch
   const RowGroup rg(W);
-  const int G = blockDim.x / (32 * W);
-  const int c = kVec * rg.t;
-  const bool on = c < a.C;
+  const int G = blockDim.x / (32 * W), nt = blockDim.x, c0 = kVec * rg.t, cs = kVec * 32 * W;
   const float inv = 1.f / a.C;
   const long long segs = (long long)a.B * a.T * a.chunks, groups = (long long)gridDim.x * G;
   const long long group = (long long)blockIdx.x * G + rg.g;
-  float mg[kVec], ma[kVec], sg[kVec], sa[kVec], sb[kVec];
+  float mg[V][kVec], ma[V][kVec], sg[V][kVec], sa[V][kVec], sb[V][kVec];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    mg[i] = 1.f;
-    ma[i] = weight && on ? __ldg(weight + c + i) : 1.f;
-    sg[i] = sa[i] = sb[i] = 0.f;
-  }
-  for (long long seg = group; seg < segs; seg += groups) {
-    const int mod = (int)(seg / a.chunks), ch = (int)(seg - (long long)mod * a.chunks);
-    const int b = mod / a.T, t = mod - b * a.T;
-    const int n0 = t * a.per + ch * a.chunk, n1 = min(n0 + a.chunk, (t + 1) * a.per);
-    if (on) {
-      if (gate) load8f(gate + b * a.gate_b + t * a.gate_t + c, mg);
-      if (scale) {
-        load8f(scale + b * a.scale_b + t * a.scale_t + c, ma);
+  for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) ma[i] += 1.f;
-      }
+    for (int i = 0; i < kVec; ++i) {
+      const int c = c0 + j * cs + i;
+      mg[j][i] = 1.f;
+      ma[j][i] = weight && c < a.C ? __ldg(weight + c) : 1.f;
+      sg[j][i] = sa[j][i] = sb[j][i] = 0.f;
     }
-    for (int n = n0; n < n1; ++n) {
-      const size_t at = ((size_t)b * a.N + n) * a.C + c;
-      Raw8<TX> xr, xd;
-      Raw8<TY> xy, xb;
-      xr.zero(); xd.zero(); xy.zero(); xb.zero();
-      if (on) {
-        xr.load(r + at);
-        xy.load(dy + at);
-        if (dr) xd.load(dr + at);
-        if (branch) xb.load(branch + at);
-      }
-      float v[kVec], g[kVec], d[kVec];
-      xr.get(v);
-      xy.get(d);
-      float s[2] = {0.f, 0.f};
+  uint4* mine = ring + threadIdx.x;
+  Cursor ahead{group, 0, 0, 0, 0};
+  ahead.open(a, segs);
+  Cursor now = ahead;
+  auto fetch = [&](int s) {
+    if (ahead.seg < segs) {
+      const size_t row = (size_t)ahead.b * a.N + ahead.n;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        g[i] = d[i] * ma[i];
-        s[0] += v[i];
-        s[1] += g[i];
+      for (int j = 0; j < V; ++j) {
+        const int c = c0 + j * cs;
+        if (c < a.C) {
+          uint4* at = mine + (s * kPieces + j * kEach) * nt;
+          copy_vec(at, nt, r + row * a.C + c);
+          copy_vec(at + kPx * nt, nt, dy + row * a.C + c);
+          if (DR) copy_vec(at + kD * nt, nt, dr + row * a.C + c);
+          if (BRANCH) copy_vec(at + kB * nt, nt, branch + row * a.C + c);
+        }
+      }
+      ahead.next(a, segs, groups);
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead - 1; ++s) fetch(s);
+  bool open = true;
+  for (int it = 0, slot = 0; now.seg < segs; ++it) {
+    const long long seg = now.seg;
+    {
+      const size_t row = (size_t)now.b * a.N + now.n;
+      if (open) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int c = c0 + j * cs;
+          if (c < a.C) {
+            if (BRANCH && gate) load8(gate + now.b * a.gate_b + now.t * a.gate_t + c, mg[j]);
+            if (scale) {
+              load8(scale + now.b * a.scale_b + now.t * a.scale_t + c, ma[j]);
+#pragma unroll
+              for (int i = 0; i < kVec; ++i) ma[j][i] += 1.f;
+            }
+          }
+        }
+      }
+      fetch(slot == 0 ? kAhead - 1 : slot - 1);
+      copy_wait<kAhead - 1>();
+      const uint4* at = mine + slot * kPieces * nt;
+      float v[V][kVec], d[V][kVec];
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (c0 + j * cs < a.C) {
+          Raw8<TX> rx;
+          Raw8<TY> ry;
+          rx.slot(at + j * kEach * nt, nt);
+          ry.slot(at + (j * kEach + kPx) * nt, nt);
+          rx.get(v[j]);
+          ry.get(d[j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) v[j][i] = d[j][i] = 0.f;
+        }
+        if (LAYER) {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            s0 += v[j][i];
+            s1 = fmaf(d[j][i], ma[j][i], s1);
+          }
+        }
       }
       float gm = 0.f;
       if (LAYER) {
-        group_sum<2>(rg, s, red[0] + rg.g * (W + 1) * 2);
-        const float mean = s[0] * inv;
-        gm = s[1] * inv;
+        const float2 s = group_sum(rg, s0, s1, sh.red[0][rg.g]);
+        const float mean = s.x * inv;
+        gm = s.y * inv;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] = on ? v[i] - mean : 0.f;
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) v[j][i] = c0 + j * cs < a.C ? v[j][i] - mean : 0.f;
       }
-      float q[2] = {0.f, 0.f};
+      float q0 = 0.f, q1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        q[0] = fmaf(v[i], v[i], q[0]);
-        q[1] = fmaf(g[i], v[i], q[1]);
-      }
-      group_sum<2>(rg, q, red[1] + rg.g * (W + 1) * 2);
-      if (!LAYER) rg.sync();           // red[1] is written again by the next row
-      const float rstd = rsqrtf(fmaf(q[0], inv, a.eps));
-      const float proj = q[1] * inv * rstd;          // mean(g * xhat)
-      float o[kVec], e[kVec];
-      xd.get(o);
-      xb.get(e);
+      for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const float xh = v[i] * rstd;
-        sa[i] = fmaf(d[i], xh, sa[i]);
-        sb[i] += d[i];
-        o[i] = fmaf(rstd, g[i] - gm - xh * proj, o[i]);
-        sg[i] = fmaf(o[i], e[i], sg[i]);
-      }
-      if (on) {
-        store8(dx + at, o);
-        if (branch) {
+        for (int i = 0; i < kVec; ++i) {
+          q0 = fmaf(v[j][i], v[j][i], q0);
+          q1 = fmaf(d[j][i] * ma[j][i], v[j][i], q1);
+        }
+      const float2 q = group_sum(rg, q0, q1, sh.red[LAYER ? 1 : it & 1][rg.g]);
+      const float rstd = rsqrtf(fmaf(q.x, inv, a.eps));
+      const float proj = q.y * inv * rstd;           // mean(g * xhat)
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) o[i] *= mg[i];
-          store8(dbranch + at, o);
+      for (int j = 0; j < V; ++j) {
+        const int c = c0 + j * cs;
+        if (c >= a.C) continue;
+        float o[kVec], e[kVec];
+        if (DR) {
+          Raw8<TX> rd;
+          rd.slot(at + (j * kEach + kD) * nt, nt);
+          rd.get(o);
+        }
+        if (BRANCH) {
+          Raw8<TY> rb;
+          rb.slot(at + (j * kEach + kB) * nt, nt);
+          rb.get(e);
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const float xh = v[j][i] * rstd;
+          sa[j][i] = fmaf(d[j][i], xh, sa[j][i]);
+          sb[j][i] += d[j][i];
+          const float in = fmaf(d[j][i], ma[j][i], -gm) - xh * proj;
+          o[i] = DR ? fmaf(rstd, in, o[i]) : rstd * in;
+          if (BRANCH) sg[j][i] = fmaf(o[i], e[i], sg[j][i]);
+        }
+        store8(dx + row * a.C + c, o);
+        if (BRANCH) {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) o[i] *= mg[j][i];
+          store8(dbranch + row * a.C + c, o);
         }
       }
     }
-    if (on && gate) {
-      store8(dgate + seg * sum_stride + c, sg);
+    slot = slot == kAhead - 1 ? 0 : slot + 1;
+    open = now.next(a, segs, groups);
+    if (!open) continue;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) sg[i] = 0.f;
-    }
-    if (on && scale) {
-      store8(dscale + seg * sum_stride + c, sa);
-      store8(dshift + seg * sum_stride + c, sb);
+    for (int j = 0; j < V; ++j) {      // the segment's sums
+      const int c = c0 + j * cs;
+      if (c >= a.C) continue;
+      if (BRANCH && gate) {
+        store8(dgate + seg * sum_stride + c, sg[j]);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) sa[i] = sb[i] = 0.f;
+        for (int i = 0; i < kVec; ++i) sg[j][i] = 0.f;
+      }
+      if (scale) {
+        store8(dscale + seg * sum_stride + c, sa[j]);
+        store8(dshift + seg * sum_stride + c, sb[j]);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sa[j][i] = sb[j][i] = 0.f;
+      }
     }
   }
-  if (weight && on) {
-    store8(wsum + group * 2 * a.C + c, sa);
-    store8(wsum + (group * 2 + 1) * a.C + c, sb);
-  }
+  copy_wait<0>();
+  if (weight)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = c0 + j * cs;
+      if (c < a.C) {
+        store8(wsum + group * 2 * a.C + c, sa[j]);
+        store8(wsum + (group * 2 + 1) * a.C + c, sb[j]);
+      }
+    }
 }
 
-// out_z[c] = sum over `parts` consecutive partial rows; a partial row holds `sums` vectors of C
-// (blockIdx.y picks one and its output), gridDim.z output rows.  Fixed order: 8 threads take
-// every eighth part, then their sums in order.
-__global__ void __launch_bounds__(256) gated_norm_reduce_kernel(const float* __restrict__ part, long long parts,
-                                                                int sums, int C, float* o0, float* o1, float* o2) {
-  __shared__ float sum[8][32];
+// Sums `parts` consecutive partial rows of `sums` vectors of C for each of gridDim.z outputs
+// rows; blockIdx.y picks the vector and its output.
+__global__ void __launch_bounds__(1024) gated_norm_reduce_kernel(const float* __restrict__ part, long long parts,
+                                                                 int sums, int C, float* o0, float* o1, float* o2) {
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   if (!out) return;
-  const int c = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
-  const float* p = part + ((size_t)blockIdx.z * parts * sums + blockIdx.y) * C;
-  float s = 0.f;
-  if (c < C)
-    for (long long i = y; i < parts; i += 8) s += p[(size_t)i * sums * C + c];
-  sum[y][threadIdx.x] = s;
-  __syncthreads();
-  if (y == 0 && c < C) {
-    for (int i = 1; i < 8; ++i) s += sum[i][threadIdx.x];
-    out[(size_t)blockIdx.z * C + c] = s;
-  }
+  column_sum(part + ((size_t)blockIdx.z * parts * sums + blockIdx.y) * C, parts, (size_t)sums * C, C, 1,
+             out + (size_t)blockIdx.z * C);
 }
 
-template <typename TX, typename TY>
-cudaError_t forward(const GatedNormArgs& a, rola_norm_kind kind, const void* x, const void* branch, const float* gate,
-                    const float* scale, const float* shift, const float* weight, const float* bias, void* r, void* y,
-                    cudaStream_t st) {
-  const RowShape s = row_shape((long long)a.B * a.N, a.C, kThreadsPerSM);
-  auto* kern = kind == ROLA_LAYER ? gated_norm_kernel<TX, TY, true> : gated_norm_kernel<TX, TY, false>;
-  kern<<<s.blocks, s.threads, 0, st>>>(a, s.W, (const TX*)x, (const TY*)branch, gate, scale, shift, weight, bias,
-                                       (TX*)r, (TY*)y);
+// Groups of a full grid, at most one per segment.
+int blocks_for(const RowShape& s, long long segs) {
+  const int per = kThreadsPerSM / s.threads;
+  const long long most = (long long)kRowSMs * (per < 1 ? 1 : per), want = (segs + s.G - 1) / s.G;
+  return (int)(want < most ? want : most);
+}
+
+template <typename K>
+cudaError_t opt_in(K kern, size_t smem) {
+  return smem <= 40 * 1024 ? cudaSuccess
+                           : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+// Rows in flight of a thread: three, or one where the rows are too wide for that.
+int rows_ahead(const RowShape& s, size_t row_bytes) { return 3 * row_bytes * s.G <= kRing ? 3 : 1; }
+
+template <typename TX, typename TY, bool LAYER, bool BRANCH, int V, int kAhead>
+cudaError_t forward_v(const GatedNormArgs& a, const RowShape& s, const void* x, const void* branch, const float* gate,
+                      const float* scale, const float* shift, const float* weight, const float* bias, void* r, void* y,
+                      cudaStream_t st) {
+  auto* kern = gated_norm_kernel<TX, TY, LAYER, BRANCH, V, kAhead>;
+  const size_t smem = 16 * (size_t)kAhead * V * (Raw8<TX>::kPieces + (BRANCH ? Raw8<TY>::kPieces : 0)) * s.threads;
+  const cudaError_t e = opt_in(kern, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<blocks_for(s, (long long)a.B * a.T * a.chunks), s.threads, smem, st>>>(
+      a, s.W, (const TX*)x, (const TY*)branch, gate, scale, shift, weight, bias, (TX*)r, (TY*)y);
   return cudaGetLastError();
 }
 
-template <typename TX, typename TY>
-cudaError_t backward(const GatedNormArgs& a, rola_norm_kind kind, const void* dy, const void* dr, const void* r,
-                     const void* branch, const float* gate, const float* scale, const float* weight, void* dx,
-                     void* dbranch, float* dgate, float* dscale, float* dshift, float* dweight, float* dbias,
-                     float* part, cudaStream_t st) {
-  const RowShape s = row_shape((long long)a.B * a.T * a.chunks, a.C, kThreadsPerSM);
-  auto* kern = kind == ROLA_LAYER ? gated_norm_backward_kernel<TX, TY, true> : gated_norm_backward_kernel<TX, TY, false>;
+template <typename TX, typename TY, typename... A>
+cudaError_t forward(const GatedNormArgs& a, rola_norm_kind kind, const void* x, const void* branch, A... rest) {
+  const RowShape s = shape_of(a.C);
+  auto go = [&](auto layer, auto with) {
+    constexpr bool L = decltype(layer)::value, B = decltype(with)::value;
+    const size_t row = 16 * (size_t)s.V * 32 * s.W * (Raw8<TX>::kPieces + (B ? Raw8<TY>::kPieces : 0));
+    if (rows_ahead(s, row) < 3)
+      return s.V == 1 ? forward_v<TX, TY, L, B, 1, 1>(a, s, x, branch, rest...)
+                      : forward_v<TX, TY, L, B, 2, 1>(a, s, x, branch, rest...);
+    return s.V == 1 ? forward_v<TX, TY, L, B, 1, 3>(a, s, x, branch, rest...)
+                    : forward_v<TX, TY, L, B, 2, 3>(a, s, x, branch, rest...);
+  };
+  using Y = std::true_type;
+  using N = std::false_type;
+  if (kind == ROLA_LAYER) return branch ? go(Y{}, Y{}) : go(Y{}, N{});
+  return branch ? go(N{}, Y{}) : go(N{}, N{});
+}
+
+template <typename TX, typename TY, bool LAYER, bool DR, bool BRANCH, int V, int kAhead>
+cudaError_t backward_v(const GatedNormArgs& a, const RowShape& s, const void* dy, const void* dr, const void* r,
+                       const void* branch, const float* gate, const float* scale, const float* weight, void* dx,
+                       void* dbranch, float* dgate, float* dscale, float* dshift, float* dweight, float* dbias,
+                       float* part, cudaStream_t st) {
+  auto* kern = gated_norm_backward_kernel<TX, TY, LAYER, DR, BRANCH, V, kAhead>;
+  constexpr int kPx = Raw8<TX>::kPieces, kPy = Raw8<TY>::kPieces;
+  const size_t smem = 16 * (size_t)kAhead * V * (kPx * (DR ? 2 : 1) + kPy * (BRANCH ? 2 : 1)) * s.threads;
+  cudaError_t e = opt_in(kern, smem);
+  if (e != cudaSuccess) return e;
   const long long mods = (long long)a.B * a.T;
+  const int blocks = blocks_for(s, mods * a.chunks);
   const bool direct = a.chunks == 1;   // a segment's sums are the gradients
   float* msum = part;
   float* wsum = part + (direct || !(gate || scale) ? 0 : mods * a.chunks * 3 * a.C);
-  kern<<<s.blocks, s.threads, 0, st>>>(
-      a, s.W, (const TY*)dy, (const TX*)dr, (const TX*)r, (const TY*)branch, gate, scale, weight, (TX*)dx,
-      (TY*)dbranch, direct ? dgate : msum, direct ? dscale : msum + a.C, direct ? dshift : msum + 2 * a.C,
-      (direct ? 1 : 3) * (int64_t)a.C, wsum);
-  cudaError_t e = cudaGetLastError();
+  kern<<<blocks, s.threads, smem, st>>>(a, s.W, (const TY*)dy, (const TX*)dr, (const TX*)r, (const TY*)branch, gate,
+                                        scale, weight, (TX*)dx, (TY*)dbranch, direct ? dgate : msum,
+                                        direct ? dscale : msum + a.C, direct ? dshift : msum + 2 * a.C,
+                                        (direct ? 1 : 3) * (int64_t)a.C, wsum);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const unsigned cols = (a.C + 31) / 32;
-  for (long long z = 0; z < mods && !direct && (gate || scale); z += 65535) {
-    const long long left = mods - z < 65535 ? mods - z : 65535;
-    auto at = [&](float* p) { return p ? p + z * a.C : nullptr; };
-    gated_norm_reduce_kernel<<<dim3(cols, 3, (unsigned)left), dim3(32, 8), 0, st>>>(
-        msum + z * a.chunks * 3 * a.C, a.chunks, 3, a.C, at(dgate), at(dscale), at(dshift));
-  }
+  if (!direct && (gate || scale))      // more than one chunk: fewer modulation rows than groups
+    gated_norm_reduce_kernel<<<dim3(cols, 3, (unsigned)mods), dim3(32, 32), 0, st>>>(msum, a.chunks, 3, a.C, dgate,
+                                                                                   dscale, dshift);
   if (weight)
-    gated_norm_reduce_kernel<<<dim3(cols, 2, 1), dim3(32, 8), 0, st>>>(wsum, (long long)s.blocks * s.G, 2, a.C, dweight,
-                                                                     dbias, nullptr);
+    gated_norm_reduce_kernel<<<dim3(cols, 2, 1), dim3(32, 32), 0, st>>>(wsum, (long long)blocks * s.G, 2, a.C, dweight,
+                                                                      dbias, nullptr);
   return cudaGetLastError();
+}
+
+template <typename TX, typename TY, typename... A>
+cudaError_t backward(const GatedNormArgs& a, rola_norm_kind kind, const void* dy, const void* dr, const void* r,
+                     const void* branch, A... rest) {
+  const RowShape s = shape_of(a.C);
+  using Y = std::true_type;
+  using N = std::false_type;
+  auto go = [&](auto layer, auto add, auto with) {
+    constexpr bool L = decltype(layer)::value, D = decltype(add)::value, B = decltype(with)::value;
+    constexpr int kPx = Raw8<TX>::kPieces, kPy = Raw8<TY>::kPieces;
+    const size_t row = 16 * (size_t)s.V * 32 * s.W * (kPx * (D ? 2 : 1) + kPy * (B ? 2 : 1));
+    if (rows_ahead(s, row) < 3)
+      return s.V == 1 ? backward_v<TX, TY, L, D, B, 1, 1>(a, s, dy, dr, r, branch, rest...)
+                      : backward_v<TX, TY, L, D, B, 2, 1>(a, s, dy, dr, r, branch, rest...);
+    return s.V == 1 ? backward_v<TX, TY, L, D, B, 1, 3>(a, s, dy, dr, r, branch, rest...)
+                    : backward_v<TX, TY, L, D, B, 2, 3>(a, s, dy, dr, r, branch, rest...);
+  };
+  auto pick = [&](auto layer) {
+    if (dr) return branch ? go(layer, Y{}, Y{}) : go(layer, Y{}, N{});
+    return branch ? go(layer, N{}, Y{}) : go(layer, N{}, N{});
+  };
+  return kind == ROLA_LAYER ? pick(Y{}) : pick(N{});
 }
 
 }  // namespace
@@ -289,10 +476,10 @@ cudaError_t backward(const GatedNormArgs& a, rola_norm_kind kind, const void* dy
 // Chunks of the tokens that share a modulation row: a segment for every group of a full grid,
 // and no more (each costs a row of partial sums).
 void gated_norm_chunks(const rola_gated_norm_params& p, int* chunks, int* chunk) {
-  const RowShape s = row_shape((long long)p.B * p.N, p.C, kThreadsPerSM);
+  const RowShape s = shape_of(p.C);
   const int per = p.N / p.T;
   const long long mods = (long long)p.B * p.T;
-  long long want = ((long long)s.blocks * s.G + mods - 1) / mods;
+  long long want = ((long long)blocks_for(s, (long long)p.B * p.N) * s.G + mods - 1) / mods;
   if (want > per) want = per;
   *chunk = (int)((per + want - 1) / want);
   *chunks = (per + *chunk - 1) / *chunk;
@@ -302,8 +489,8 @@ size_t gated_norm_workspace(const rola_gated_norm_params& p) {
   int chunks, chunk;
   gated_norm_chunks(p, &chunks, &chunk);
   const long long segs = (long long)p.B * p.T * chunks;
-  const RowShape s = row_shape(segs, p.C, kThreadsPerSM);
-  return sizeof(float) * (size_t)p.C * ((chunks > 1 ? 3 * segs : 0) + 2 * (long long)s.blocks * s.G);
+  const RowShape s = shape_of(p.C);
+  return sizeof(float) * (size_t)p.C * ((chunks > 1 ? 3 * segs : 0) + 2 * (long long)blocks_for(s, segs) * s.G);
 }
 
 cudaError_t launch_gated_norm(const GatedNormArgs& a, rola_dtype xt, rola_dtype yt, rola_norm_kind kind, const void* x,

@@ -1,32 +1,37 @@
-// Building blocks of the kernels that work on whole token rows (norms, rotary positions): a
-// row is owned by a group of W warps, every thread of which holds the same 8 channels of each
-// row it meets.
+// Building blocks of the kernels that work on whole token rows (norms, rotary positions).  A row
+// is owned by a group of W warps; thread t of the group holds V vectors of 8 channels of every
+// row it meets: t, t + 32 W, ...  Rows to come are fetched by asynchronous copies into slots of
+// shared memory that only the thread itself reads, so that fetching ahead costs neither registers
+// nor barriers.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "sm100_ptx.cuh"
+
 namespace rola {
 
-constexpr int kVec = 8;              // channels of a thread
+constexpr int kVec = 8;              // channels of a vector
 constexpr int kMaxRowChannels = 8192;
-constexpr int kMaxRowWarps = kMaxRowChannels / kVec / 32;
+constexpr int kMaxRowWarps = 8;      // of a group: 8192 channels at V = 4
 constexpr int kRowSMs = 148;
 
-// Shape of a launch over rows of C channels: W warps own a row, a block holds G such groups.
+// Threads of a row: W warps with V vectors each.  More vectors per thread mean fewer threads to
+// reduce over; among the V whose last warp is not much emptier, the largest is taken.
 struct RowShape {
-  int W, G, threads, blocks;
+  int V, W, G, threads;   // G groups in a block
 };
-inline RowShape row_shape(long long rows, int C, int threads_per_sm) {
-  RowShape s;
-  s.W = (C / kVec + 31) / 32;
-  s.G = s.W >= 8 ? 1 : 8 / s.W;
+inline RowShape row_shape(int C, int max_v, int max_warps = kMaxRowWarps) {
+  const int vecs = C / kVec;
+  RowShape s{1, (vecs + 31) / 32, 1, 0};
+  for (int v = 2; v <= max_v; v *= 2) {
+    const int w = (vecs + 32 * v - 1) / (32 * v);
+    if (s.W > max_warps || 8ll * v * w <= 9ll * s.V * s.W) s.V = v, s.W = w;
+  }
+  s.G = s.W >= 4 ? 1 : 4 / s.W;
   s.threads = 32 * s.W * s.G;
-  long long want = (rows + s.G - 1) / s.G;
-  int per_sm = threads_per_sm / s.threads;
-  const long long most = (long long)kRowSMs * (per_sm < 1 ? 1 : per_sm);
-  s.blocks = (int)(want < most ? want : most);
   return s;
 }
 
@@ -34,9 +39,10 @@ template <typename T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
+  static constexpr int kPieces = 1;   // 16-byte pieces of a vector
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void slot(const uint4* s, int) { a = *s; }
   __device__ __forceinline__ void get(float* v) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -48,12 +54,16 @@ struct Raw8<__nv_bfloat16> {
 };
 template <>
 struct Raw8<float> {
+  static constexpr int kPieces = 2;
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
     a = *reinterpret_cast<const float4*>(p);
     b = *reinterpret_cast<const float4*>(p + 4);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void slot(const uint4* s, int stride) {
+    a = *reinterpret_cast<const float4*>(s);
+    b = *reinterpret_cast<const float4*>(s + stride);
+  }
   __device__ __forceinline__ void get(float* v) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -73,6 +83,27 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
 __device__ __forceinline__ void store8(float* p, const float* v) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  Raw8<float> r;
+  r.load(p);
+  r.get(v);
+}
+
+// Asynchronous 16-byte copies, waited for in groups: `keep` groups may still be in flight.
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int keep>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(keep) : "memory");
+}
+// A vector of T into the thread's slot (pieces `stride` slots apart).
+template <typename T>
+__device__ __forceinline__ void copy_vec(uint4* slot, int stride, const T* src) {
+#pragma unroll
+  for (int p = 0; p < Raw8<T>::kPieces; ++p) copy16(slot + p * stride, reinterpret_cast<const uint4*>(src) + p);
 }
 
 // A thread's place in its group.
@@ -94,29 +125,61 @@ struct RowGroup {
   }
 };
 
-// Sums of NV values over the group, to every thread, in a fixed order: a butterfly in each
-// warp, then the warps' sums one after the other.  `buf` is [kMaxRowWarps][NV] of the group;
-// two reductions in a row use two buffers (one barrier then keeps them apart).
-template <int NV>
-__device__ __forceinline__ void group_sum(const RowGroup& rg, float (&v)[NV], float* buf) {
+// Sums over the group, to every thread, in a fixed order: a butterfly in each warp (two values
+// share one: each half of the lanes goes on with one of them), then the warps' sums one after
+// the other.  A barrier as well.  `buf` holds W values (pairs) of the group; two
+// reductions in a row use two buffers.
+__device__ __forceinline__ float group_sum(const RowGroup& rg, float v, float* buf) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (rg.W == 1) {
     __syncwarp();
-    return;
+    return v;
   }
-  if (rg.lane == 0)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) buf[rg.wi * NV + i] = v[i];
+  if (rg.lane == 0) buf[rg.wi] = v;
   rg.sync();
+  v = buf[0];
+  for (int w = 1; w < rg.W; ++w) v += buf[w];
+  return v;
+}
+__device__ __forceinline__ float2 group_sum(const RowGroup& rg, float a, float b, float* buf) {
+  const bool low = rg.lane < 16;
+  float v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = rg.lane < rg.W ? buf[rg.lane * NV + i] : 0.f;
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (rg.W == 1) return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
+  if ((rg.lane & 15) == 0) buf[2 * rg.wi + (rg.lane >> 4)] = v;
+  rg.sync();
+  const float2* p = reinterpret_cast<const float2*>(buf);
+  float2 s = p[0];
+  for (int w = 1; w < rg.W; ++w) {
+    s.x += p[w].x;
+    s.y += p[w].y;
+  }
+  return s;
+}
+
+// out[c] = sum over `parts` partial rows, `stride` floats apart, of the `fold` columns c, c + cols,
+// ... : 32 threads take every 32nd part, then a fixed tree.  A block has 32 columns x 32 threads.
+__device__ __forceinline__ void column_sum(const float* __restrict__ part, long long parts, size_t stride, int cols,
+                                           int fold, float* __restrict__ out) {
+  __shared__ float sum[32][33];
+  const int col = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
+  float s = 0.f;
+  if (col < cols) {
+    for (int f = 0; f < fold; ++f) {
+      const float* p = part + col + (size_t)f * cols;
+#pragma unroll 8
+      for (long long i = y; i < parts; i += 32) s += p[(size_t)i * stride];
+    }
+  }
+  sum[y][threadIdx.x] = s;
+  __syncthreads();
+  s = sum[threadIdx.x][y];             // column y of the block, part lane threadIdx.x
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int at = blockIdx.x * 32 + y;
+  if (threadIdx.x == 0 && at < cols) out[at] = s;
 }
 
 }  // namespace rola
