@@ -54,12 +54,9 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
   const int b = (int)(bn / padded), n = (int)(bn - (long long)b * padded);
   float s = 0.f;
   if (b < a.B && n < a.Nq) {
-    Raw8<__nv_bfloat16> x, y;
-    x.load(dout + b * a.dout.b + n * a.dout.n + h * a.dout.h + c);
-    y.load(out + (((size_t)b * a.Nq + n) * a.H + h) * D + c);
     float u[kVec], v[kVec];
-    x.get(u);
-    y.get(v);
+    load8(dout + b * a.dout.b + n * a.dout.n + h * a.dout.h + c, u);
+    load8(out + (((size_t)b * a.Nq + n) * a.H + h) * D + c, v);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) s = fmaf(u[i], v[i], s);
   }

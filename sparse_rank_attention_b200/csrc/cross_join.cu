@@ -32,10 +32,8 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
     const float w = expf(__ldg(plse + s * zs + zat) - ref);
     sum += w;
     if (w == 0.f) continue;            // a part without a valid key holds zeros
-    Raw8<float> r;
     float v[kVec];
-    r.load(part + ((size_t)s * rows + row) * a.d + c);
-    r.get(v);
+    load8(part + ((size_t)s * rows + row) * a.d + c, v);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) acc[i] = fmaf(w, v[i], acc[i]);
   }
@@ -53,10 +51,8 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(int parts, size_t n, siz
   if (at >= n) return;
   float acc[kVec] = {};
   for (int s = 0; s < parts; ++s) {
-    Raw8<float> r;
     float v[kVec];
-    r.load(part + s * stride + at);
-    r.get(v);
+    load8(part + s * stride + at, v);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) acc[i] += v[i];
   }

@@ -7,7 +7,7 @@
 //   the sums over the tokens that share a row of the modulation (all tokens for weight, bias).
 //
 // Bound by memory: each tensor is read or written once.  A group of warps owns a token; a thread
-// has the same vectors of 8 channels of every token it meets, so that the modulation stays in
+// has the same pieces of E channels of every token it meets, so that the modulation stays in
 // registers while the tokens share it and the column sums of the backward are private to a
 // thread.  The variance is taken about the mean of the values held in registers (a second sum,
 // not E[x^2] - E[x]^2, which loses everything when the mean is large).
@@ -22,7 +22,6 @@ namespace {
 constexpr int kThreadsPerSM = 1024;   // resident threads that a grid is sized for
 constexpr size_t kRing = 192 * 1024;  // shared memory for the rows in flight of a block
 constexpr int kMaxGroups = 4;
-constexpr int kMaxV = 2;              // vectors of a thread
 constexpr int kMaxThreads = 512;      // 8192 channels
 constexpr int kMaxWarps = kMaxThreads / 32;
 
@@ -30,7 +29,9 @@ struct Shared {
   alignas(16) float red[2][kMaxGroups][2 * kMaxWarps];
 };
 
-RowShape shape_of(int C) { return row_shape(C, kMaxV, kMaxWarps); }
+// Channels of a piece; pieces of 8 go by two, pieces of 4 by four.
+constexpr int piece_of(rola_dtype x, rola_dtype y) { return x == ROLA_F32 || y == ROLA_F32 ? 4 : 8; }
+RowShape shape_of(int C, int E) { return row_shape(C, E, 16 / E, kMaxWarps); }
 
 // A group's walk over its rows: the tokens of segment `seg`, then of seg + groups, ...; a segment
 // is a chunk of the tokens that share a modulation row.
@@ -54,29 +55,28 @@ struct Cursor {
   }
 };
 
-template <typename TX, typename TY, bool LAYER, bool BRANCH, int V, int kAhead>
+template <typename TX, typename TY, int E, bool LAYER, bool BRANCH, int V, int kAhead>
 __global__ void __launch_bounds__(kMaxThreads) gated_norm_kernel(
     const __grid_constant__ GatedNormArgs a, int W, const TX* x, const TY* __restrict__ branch,
     const float* __restrict__ gate, const float* __restrict__ scale, const float* __restrict__ shift,
     const float* __restrict__ weight, const float* __restrict__ bias, TX* r, TY* __restrict__ y) {
-  constexpr int kPx = Raw8<TX>::kPieces, kPb = BRANCH ? Raw8<TY>::kPieces : 0, kPieces = V * (kPx + kPb);
+  constexpr int kBx = piece_bytes<E, TX>(), kBb = BRANCH ? piece_bytes<E, TY>() : 0, kRow = V * (kBx + kBb);
   __shared__ Shared sh;
-  extern __shared__ uint4 ring[];      // [kAhead][pieces][threads]
+  extern __shared__ __align__(16) uint8_t ring[];   // [kAhead][V][x, branch][threads] pieces
   const RowGroup rg(W);
-  const int G = blockDim.x / (32 * W), nt = blockDim.x, c0 = kVec * rg.t, cs = kVec * 32 * W;
+  const int G = blockDim.x / (32 * W), nt = blockDim.x, c0 = E * rg.t, cs = E * 32 * W;
   const float inv = 1.f / a.C;
   const long long segs = (long long)a.B * a.T * a.chunks, groups = (long long)gridDim.x * G;
-  float mg[V][kVec], ma[V][kVec], mb[V][kVec];
+  float mg[V][E], ma[V][E], mb[V][E];
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < E; ++i) {
       const int c = c0 + j * cs + i;
       mg[j][i] = 1.f;
       ma[j][i] = weight && c < a.C ? __ldg(weight + c) : 1.f;
       mb[j][i] = bias && c < a.C ? __ldg(bias + c) : 0.f;
     }
-  uint4* mine = ring + threadIdx.x;
   Cursor ahead{(long long)blockIdx.x * G + rg.g, 0, 0, 0, 0};
   ahead.open(a, segs);
   Cursor now = ahead;
@@ -87,9 +87,9 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_kernel(
       for (int j = 0; j < V; ++j) {
         const int c = c0 + j * cs;
         if (c < a.C) {
-          uint4* at = mine + (s * kPieces + j * (kPx + kPb)) * nt;
-          copy_vec(at, nt, x + row * a.C + c);
-          if (BRANCH) copy_vec(at + kPx * nt, nt, branch + row * a.C + c);
+          uint8_t* at = ring + (s * kRow + j * (kBx + kBb)) * nt;
+          fetch_piece<E>(at, x + row * a.C + c);
+          if (BRANCH) fetch_piece<E>(at + kBx * nt, branch + row * a.C + c);
         }
       }
       ahead.next(a, segs, groups);
@@ -107,44 +107,40 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_kernel(
         for (int j = 0; j < V; ++j) {
           const int c = c0 + j * cs;
           if (c < a.C) {
-            if (gate) load8(gate + now.b * a.gate_b + now.t * a.gate_t + c, mg[j]);
+            if (gate) load_floats<E>(gate + now.b * a.gate_b + now.t * a.gate_t + c, mg[j]);
             if (scale) {
-              load8(scale + now.b * a.scale_b + now.t * a.scale_t + c, ma[j]);
-              load8(shift + now.b * a.shift_b + now.t * a.shift_t + c, mb[j]);
+              load_floats<E>(scale + now.b * a.scale_b + now.t * a.scale_t + c, ma[j]);
+              load_floats<E>(shift + now.b * a.shift_b + now.t * a.shift_t + c, mb[j]);
 #pragma unroll
-              for (int i = 0; i < kVec; ++i) ma[j][i] += 1.f;
+              for (int i = 0; i < E; ++i) ma[j][i] += 1.f;
             }
           }
         }
       }
       fetch(slot == 0 ? kAhead - 1 : slot - 1);
       copy_wait<kAhead - 1>();
-      float v[V][kVec];
+      float v[V][E];
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = c0 + j * cs;
-        const uint4* at = mine + (slot * kPieces + j * (kPx + kPb)) * nt;
+        const uint8_t* at = ring + (slot * kRow + j * (kBx + kBb)) * nt;
         if (c < a.C) {
-          Raw8<TX> rx;
-          rx.slot(at, nt);
-          rx.get(v[j]);
+          read_piece<E, TX>(at, v[j]);
           if (BRANCH) {
-            Raw8<TY> rb;
-            float u[kVec];
-            rb.slot(at + kPx * nt, nt);
-            rb.get(u);
+            float u[E];
+            read_piece<E, TY>(at + kBx * nt, u);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[j][i] = fmaf(mg[j][i], u[i], v[j][i]);
-            store8(r + row * a.C + c, v[j]);
+            for (int i = 0; i < E; ++i) v[j][i] = fmaf(mg[j][i], u[i], v[j][i]);
+            store_piece<E>(r + row * a.C + c, v[j]);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) v[j][i] = 0.f;
+          for (int i = 0; i < E; ++i) v[j][i] = 0.f;
         }
         if (LAYER) {
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) sum += v[j][i];
+          for (int i = 0; i < E; ++i) sum += v[j][i];
         }
       }
       if (LAYER) {
@@ -152,21 +148,21 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_kernel(
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) v[j][i] = c0 + j * cs < a.C ? v[j][i] - mean : 0.f;
+          for (int i = 0; i < E; ++i) v[j][i] = c0 + j * cs < a.C ? v[j][i] - mean : 0.f;
       }
       float sq = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sq = fmaf(v[j][i], v[j][i], sq);
+        for (int i = 0; i < E; ++i) sq = fmaf(v[j][i], v[j][i], sq);
       const float rstd = rsqrtf(fmaf(group_sum(rg, sq, sh.red[LAYER ? 1 : it & 1][rg.g]), inv, a.eps));
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = c0 + j * cs;
         if (c < a.C) {
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) v[j][i] = fmaf(v[j][i] * rstd, ma[j][i], mb[j][i]);
-          store8(y + row * a.C + c, v[j]);
+          for (int i = 0; i < E; ++i) v[j][i] = fmaf(v[j][i] * rstd, ma[j][i], mb[j][i]);
+          store_piece<E>(y + row * a.C + c, v[j]);
         }
       }
     }
@@ -180,33 +176,32 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_kernel(
 // row.  A segment's column sums go to msum, [segments][3][C] (dgate, dscale, dshift): the
 // gradients themselves where a modulation row is one segment (outputs given), else partial
 // sums.  The sums of weight and bias run over all segments of the group: wsum [groups][2][C].
-template <typename TX, typename TY, bool LAYER, bool DR, bool BRANCH, int V, int kAhead>
-__global__ void __launch_bounds__(kMaxThreads) gated_norm_backward_kernel(
+template <typename TX, typename TY, int E, bool LAYER, bool DR, bool BRANCH, int V, int kAhead, int kMost>
+__global__ void __launch_bounds__(kMost) gated_norm_backward_kernel(
     const __grid_constant__ GatedNormArgs a, int W, const TY* __restrict__ dy, const TX* dr,
     const TX* __restrict__ r, const TY* __restrict__ branch, const float* __restrict__ gate,
     const float* __restrict__ scale, const float* __restrict__ weight, TX* dx, TY* __restrict__ dbranch,
     float* __restrict__ dgate, float* __restrict__ dscale, float* __restrict__ dshift, int64_t sum_stride,
     float* __restrict__ wsum) {
-  constexpr int kPx = Raw8<TX>::kPieces, kPy = Raw8<TY>::kPieces;
-  constexpr int kD = kPx + kPy, kB = kD + (DR ? kPx : 0), kEach = kB + (BRANCH ? kPy : 0), kPieces = V * kEach;
+  constexpr int kBx = piece_bytes<E, TX>(), kBy = piece_bytes<E, TY>();
+  constexpr int kD = kBx + kBy, kB = kD + (DR ? kBx : 0), kEach = kB + (BRANCH ? kBy : 0), kRow = V * kEach;
   __shared__ Shared sh;
-  extern __shared__ uint4 ring[];      // [kAhead][pieces][threads]: r, dy, dr, branch
+  extern __shared__ __align__(16) uint8_t ring[];   // [kAhead][V][r, dy, dr, branch][threads] pieces
   const RowGroup rg(W);
-  const int G = blockDim.x / (32 * W), nt = blockDim.x, c0 = kVec * rg.t, cs = kVec * 32 * W;
+  const int G = blockDim.x / (32 * W), nt = blockDim.x, c0 = E * rg.t, cs = E * 32 * W;
   const float inv = 1.f / a.C;
   const long long segs = (long long)a.B * a.T * a.chunks, groups = (long long)gridDim.x * G;
   const long long group = (long long)blockIdx.x * G + rg.g;
-  float mg[V][kVec], ma[V][kVec], sg[V][kVec], sa[V][kVec], sb[V][kVec];
+  float mg[V][E], ma[V][E], sg[V][E], sa[V][E], sb[V][E];
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < E; ++i) {
       const int c = c0 + j * cs + i;
       mg[j][i] = 1.f;
       ma[j][i] = weight && c < a.C ? __ldg(weight + c) : 1.f;
       sg[j][i] = sa[j][i] = sb[j][i] = 0.f;
     }
-  uint4* mine = ring + threadIdx.x;
   Cursor ahead{group, 0, 0, 0, 0};
   ahead.open(a, segs);
   Cursor now = ahead;
@@ -217,11 +212,11 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_backward_kernel(
       for (int j = 0; j < V; ++j) {
         const int c = c0 + j * cs;
         if (c < a.C) {
-          uint4* at = mine + (s * kPieces + j * kEach) * nt;
-          copy_vec(at, nt, r + row * a.C + c);
-          copy_vec(at + kPx * nt, nt, dy + row * a.C + c);
-          if (DR) copy_vec(at + kD * nt, nt, dr + row * a.C + c);
-          if (BRANCH) copy_vec(at + kB * nt, nt, branch + row * a.C + c);
+          uint8_t* at = ring + (s * kRow + j * kEach) * nt;
+          fetch_piece<E>(at, r + row * a.C + c);
+          fetch_piece<E>(at + kBx * nt, dy + row * a.C + c);
+          if (DR) fetch_piece<E>(at + kD * nt, dr + row * a.C + c);
+          if (BRANCH) fetch_piece<E>(at + kB * nt, branch + row * a.C + c);
         }
       }
       ahead.next(a, segs, groups);
@@ -240,36 +235,32 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_backward_kernel(
         for (int j = 0; j < V; ++j) {
           const int c = c0 + j * cs;
           if (c < a.C) {
-            if (BRANCH && gate) load8(gate + now.b * a.gate_b + now.t * a.gate_t + c, mg[j]);
+            if (BRANCH && gate) load_floats<E>(gate + now.b * a.gate_b + now.t * a.gate_t + c, mg[j]);
             if (scale) {
-              load8(scale + now.b * a.scale_b + now.t * a.scale_t + c, ma[j]);
+              load_floats<E>(scale + now.b * a.scale_b + now.t * a.scale_t + c, ma[j]);
 #pragma unroll
-              for (int i = 0; i < kVec; ++i) ma[j][i] += 1.f;
+              for (int i = 0; i < E; ++i) ma[j][i] += 1.f;
             }
           }
         }
       }
       fetch(slot == 0 ? kAhead - 1 : slot - 1);
       copy_wait<kAhead - 1>();
-      const uint4* at = mine + slot * kPieces * nt;
-      float v[V][kVec], d[V][kVec];
+      const uint8_t* at = ring + slot * kRow * nt;
+      float v[V][E], d[V][E];
       float s0 = 0.f, s1 = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         if (c0 + j * cs < a.C) {
-          Raw8<TX> rx;
-          Raw8<TY> ry;
-          rx.slot(at + j * kEach * nt, nt);
-          ry.slot(at + (j * kEach + kPx) * nt, nt);
-          rx.get(v[j]);
-          ry.get(d[j]);
+          read_piece<E, TX>(at + j * kEach * nt, v[j]);
+          read_piece<E, TY>(at + (j * kEach + kBx) * nt, d[j]);
         } else {
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) v[j][i] = d[j][i] = 0.f;
+          for (int i = 0; i < E; ++i) v[j][i] = d[j][i] = 0.f;
         }
         if (LAYER) {
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) {
+          for (int i = 0; i < E; ++i) {
             s0 += v[j][i];
             s1 = fmaf(d[j][i], ma[j][i], s1);
           }
@@ -283,13 +274,13 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_backward_kernel(
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) v[j][i] = c0 + j * cs < a.C ? v[j][i] - mean : 0.f;
+          for (int i = 0; i < E; ++i) v[j][i] = c0 + j * cs < a.C ? v[j][i] - mean : 0.f;
       }
       float q0 = 0.f, q1 = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
+        for (int i = 0; i < E; ++i) {
           q0 = fmaf(v[j][i], v[j][i], q0);
           q1 = fmaf(d[j][i] * ma[j][i], v[j][i], q1);
         }
@@ -300,19 +291,11 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_backward_kernel(
       for (int j = 0; j < V; ++j) {
         const int c = c0 + j * cs;
         if (c >= a.C) continue;
-        float o[kVec], e[kVec];
-        if (DR) {
-          Raw8<TX> rd;
-          rd.slot(at + (j * kEach + kD) * nt, nt);
-          rd.get(o);
-        }
-        if (BRANCH) {
-          Raw8<TY> rb;
-          rb.slot(at + (j * kEach + kB) * nt, nt);
-          rb.get(e);
-        }
+        float o[E], e[E];
+        if (DR) read_piece<E, TX>(at + (j * kEach + kD) * nt, o);
+        if (BRANCH) read_piece<E, TY>(at + (j * kEach + kB) * nt, e);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
+        for (int i = 0; i < E; ++i) {
           const float xh = v[j][i] * rstd;
           sa[j][i] = fmaf(d[j][i], xh, sa[j][i]);
           sb[j][i] += d[j][i];
@@ -320,11 +303,11 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_backward_kernel(
           o[i] = DR ? fmaf(rstd, in, o[i]) : rstd * in;
           if (BRANCH) sg[j][i] = fmaf(o[i], e[i], sg[j][i]);
         }
-        store8(dx + row * a.C + c, o);
+        store_piece<E>(dx + row * a.C + c, o);
         if (BRANCH) {
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) o[i] *= mg[j][i];
-          store8(dbranch + row * a.C + c, o);
+          for (int i = 0; i < E; ++i) o[i] *= mg[j][i];
+          store_piece<E>(dbranch + row * a.C + c, o);
         }
       }
     }
@@ -336,15 +319,15 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_backward_kernel(
       const int c = c0 + j * cs;
       if (c >= a.C) continue;
       if (BRANCH && gate) {
-        store8(dgate + seg * sum_stride + c, sg[j]);
+        store_floats<E>(dgate + seg * sum_stride + c, sg[j]);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sg[j][i] = 0.f;
+        for (int i = 0; i < E; ++i) sg[j][i] = 0.f;
       }
       if (scale) {
-        store8(dscale + seg * sum_stride + c, sa[j]);
-        store8(dshift + seg * sum_stride + c, sb[j]);
+        store_floats<E>(dscale + seg * sum_stride + c, sa[j]);
+        store_floats<E>(dshift + seg * sum_stride + c, sb[j]);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sa[j][i] = sb[j][i] = 0.f;
+        for (int i = 0; i < E; ++i) sa[j][i] = sb[j][i] = 0.f;
       }
     }
   }
@@ -354,8 +337,8 @@ __global__ void __launch_bounds__(kMaxThreads) gated_norm_backward_kernel(
     for (int j = 0; j < V; ++j) {
       const int c = c0 + j * cs;
       if (c < a.C) {
-        store8(wsum + group * 2 * a.C + c, sa[j]);
-        store8(wsum + (group * 2 + 1) * a.C + c, sb[j]);
+        store_floats<E>(wsum + group * 2 * a.C + c, sa[j]);
+        store_floats<E>(wsum + (group * 2 + 1) * a.C + c, sb[j]);
       }
     }
 }
@@ -383,15 +366,12 @@ cudaError_t opt_in(K kern, size_t smem) {
                            : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
-// Rows in flight of a thread: three, or one where the rows are too wide for that.
-int rows_ahead(const RowShape& s, size_t row_bytes) { return 3 * row_bytes * s.G <= kRing ? 3 : 1; }
-
-template <typename TX, typename TY, bool LAYER, bool BRANCH, int V, int kAhead>
+template <typename TX, typename TY, int E, bool LAYER, bool BRANCH, int V, int kAhead>
 cudaError_t forward_v(const GatedNormArgs& a, const RowShape& s, const void* x, const void* branch, const float* gate,
                       const float* scale, const float* shift, const float* weight, const float* bias, void* r, void* y,
                       cudaStream_t st) {
-  auto* kern = gated_norm_kernel<TX, TY, LAYER, BRANCH, V, kAhead>;
-  const size_t smem = 16 * (size_t)kAhead * V * (Raw8<TX>::kPieces + (BRANCH ? Raw8<TY>::kPieces : 0)) * s.threads;
+  auto* kern = gated_norm_kernel<TX, TY, E, LAYER, BRANCH, V, kAhead>;
+  const size_t smem = (size_t)kAhead * V * (piece_bytes<E, TX>() + (BRANCH ? piece_bytes<E, TY>() : 0)) * s.threads;
   const cudaError_t e = opt_in(kern, smem);
   if (e != cudaSuccess) return e;
   kern<<<blocks_for(s, (long long)a.B * a.T * a.chunks), s.threads, smem, st>>>(
@@ -399,17 +379,25 @@ cudaError_t forward_v(const GatedNormArgs& a, const RowShape& s, const void* x, 
   return cudaGetLastError();
 }
 
+// Calls go with the shape's V and, where three rows of it fit, kAhead = 3, as constants.
+template <int E, typename F>
+cudaError_t with_shape(const RowShape& s, int row_bytes, const F& go) {
+  const bool deep = 3ull * row_bytes * s.V * s.threads <= kRing;
+  auto pick = [&](auto v) { return deep ? go(v, std::integral_constant<int, 3>{}) : go(v, std::integral_constant<int, 1>{}); };
+  if constexpr (E == 4)
+    if (s.V == 4) return pick(std::integral_constant<int, 4>{});
+  return s.V == 2 ? pick(std::integral_constant<int, 2>{}) : pick(std::integral_constant<int, 1>{});
+}
+
 template <typename TX, typename TY, typename... A>
 cudaError_t forward(const GatedNormArgs& a, rola_norm_kind kind, const void* x, const void* branch, A... rest) {
-  const RowShape s = shape_of(a.C);
+  constexpr int E = sizeof(TX) == 4 ? 4 : 8;
+  const RowShape s = shape_of(a.C, E);
   auto go = [&](auto layer, auto with) {
     constexpr bool L = decltype(layer)::value, B = decltype(with)::value;
-    const size_t row = 16 * (size_t)s.V * 32 * s.W * (Raw8<TX>::kPieces + (B ? Raw8<TY>::kPieces : 0));
-    if (rows_ahead(s, row) < 3)
-      return s.V == 1 ? forward_v<TX, TY, L, B, 1, 1>(a, s, x, branch, rest...)
-                      : forward_v<TX, TY, L, B, 2, 1>(a, s, x, branch, rest...);
-    return s.V == 1 ? forward_v<TX, TY, L, B, 1, 3>(a, s, x, branch, rest...)
-                    : forward_v<TX, TY, L, B, 2, 3>(a, s, x, branch, rest...);
+    return with_shape<E>(s, piece_bytes<E, TX>() + (B ? piece_bytes<E, TY>() : 0), [&](auto v, auto ahead) {
+      return forward_v<TX, TY, E, L, B, decltype(v)::value, decltype(ahead)::value>(a, s, x, branch, rest...);
+    });
   };
   using Y = std::true_type;
   using N = std::false_type;
@@ -417,14 +405,14 @@ cudaError_t forward(const GatedNormArgs& a, rola_norm_kind kind, const void* x, 
   return branch ? go(N{}, Y{}) : go(N{}, N{});
 }
 
-template <typename TX, typename TY, bool LAYER, bool DR, bool BRANCH, int V, int kAhead>
+template <typename TX, typename TY, int E, bool LAYER, bool DR, bool BRANCH, int V, int kAhead, int kMost>
 cudaError_t backward_v(const GatedNormArgs& a, const RowShape& s, const void* dy, const void* dr, const void* r,
                        const void* branch, const float* gate, const float* scale, const float* weight, void* dx,
                        void* dbranch, float* dgate, float* dscale, float* dshift, float* dweight, float* dbias,
                        float* part, cudaStream_t st) {
-  auto* kern = gated_norm_backward_kernel<TX, TY, LAYER, DR, BRANCH, V, kAhead>;
-  constexpr int kPx = Raw8<TX>::kPieces, kPy = Raw8<TY>::kPieces;
-  const size_t smem = 16 * (size_t)kAhead * V * (kPx * (DR ? 2 : 1) + kPy * (BRANCH ? 2 : 1)) * s.threads;
+  auto* kern = gated_norm_backward_kernel<TX, TY, E, LAYER, DR, BRANCH, V, kAhead, kMost>;
+  constexpr int kBx = piece_bytes<E, TX>(), kBy = piece_bytes<E, TY>();
+  const size_t smem = (size_t)kAhead * V * (kBx * (DR ? 2 : 1) + kBy * (BRANCH ? 2 : 1)) * s.threads;
   cudaError_t e = opt_in(kern, smem);
   if (e != cudaSuccess) return e;
   const long long mods = (long long)a.B * a.T;
@@ -451,18 +439,18 @@ cudaError_t backward_v(const GatedNormArgs& a, const RowShape& s, const void* dy
 template <typename TX, typename TY, typename... A>
 cudaError_t backward(const GatedNormArgs& a, rola_norm_kind kind, const void* dy, const void* dr, const void* r,
                      const void* branch, A... rest) {
-  const RowShape s = shape_of(a.C);
+  constexpr int E = sizeof(TX) == 4 ? 4 : 8, kBx = piece_bytes<E, TX>(), kBy = piece_bytes<E, TY>();
+  const RowShape s = shape_of(a.C, E);
   using Y = std::true_type;
   using N = std::false_type;
   auto go = [&](auto layer, auto add, auto with) {
     constexpr bool L = decltype(layer)::value, D = decltype(add)::value, B = decltype(with)::value;
-    constexpr int kPx = Raw8<TX>::kPieces, kPy = Raw8<TY>::kPieces;
-    const size_t row = 16 * (size_t)s.V * 32 * s.W * (kPx * (D ? 2 : 1) + kPy * (B ? 2 : 1));
-    if (rows_ahead(s, row) < 3)
-      return s.V == 1 ? backward_v<TX, TY, L, D, B, 1, 1>(a, s, dy, dr, r, branch, rest...)
-                      : backward_v<TX, TY, L, D, B, 2, 1>(a, s, dy, dr, r, branch, rest...);
-    return s.V == 1 ? backward_v<TX, TY, L, D, B, 1, 3>(a, s, dy, dr, r, branch, rest...)
-                    : backward_v<TX, TY, L, D, B, 2, 3>(a, s, dy, dr, r, branch, rest...);
+    return with_shape<E>(s, kBx * (D ? 2 : 1) + kBy * (B ? 2 : 1), [&](auto v, auto ahead) {
+      constexpr int V = decltype(v)::value, kAhead = decltype(ahead)::value;
+      // 320 threads (5120 channels) leave a thread 200 registers, 512 leave 128
+      return s.threads <= 320 ? backward_v<TX, TY, E, L, D, B, V, kAhead, 320>(a, s, dy, dr, r, branch, rest...)
+                              : backward_v<TX, TY, E, L, D, B, V, kAhead, kMaxThreads>(a, s, dy, dr, r, branch, rest...);
+    });
   };
   auto pick = [&](auto layer) {
     if (dr) return branch ? go(layer, Y{}, Y{}) : go(layer, Y{}, N{});
@@ -476,7 +464,7 @@ cudaError_t backward(const GatedNormArgs& a, rola_norm_kind kind, const void* dy
 // Chunks of the tokens that share a modulation row: a segment for every group of a full grid,
 // and no more (each costs a row of partial sums).
 void gated_norm_chunks(const rola_gated_norm_params& p, int* chunks, int* chunk) {
-  const RowShape s = shape_of(p.C);
+  const RowShape s = shape_of(p.C, piece_of(p.x_dtype, p.y_dtype));
   const int per = p.N / p.T;
   const long long mods = (long long)p.B * p.T;
   long long want = ((long long)blocks_for(s, (long long)p.B * p.N) * s.G + mods - 1) / mods;
@@ -489,7 +477,7 @@ size_t gated_norm_workspace(const rola_gated_norm_params& p) {
   int chunks, chunk;
   gated_norm_chunks(p, &chunks, &chunk);
   const long long segs = (long long)p.B * p.T * chunks;
-  const RowShape s = shape_of(p.C);
+  const RowShape s = shape_of(p.C, piece_of(p.x_dtype, p.y_dtype));
   return sizeof(float) * (size_t)p.C * ((chunks > 1 ? 3 * segs : 0) + 2 * (long long)blocks_for(s, segs) * s.G);
 }
 

@@ -6,8 +6,8 @@
 //
 // Bound by memory: every element is read once and written once, so a token's row stays in
 // registers between the statistics and the rotation.  A group of warps owns the rows of one
-// tensor (q or k); a thread has up to four vectors of 8 channels, at the same channels of their
-// heads (a group's width is a multiple of the head), so that one set of four angles serves them
+// tensor (q or k); a thread has up to four pieces of E channels, at the same channels of their
+// heads (a group's width is a multiple of the head), so that one set of E/2 angles serves them
 // all and 1/rms is folded into it.  A token's d/2 angles are formed one token ahead by the first
 // threads of the group: the angle in fp64 turns, reduced to one turn (exact to 2^-53 of the
 // position), then sincospi in fp32.
@@ -23,10 +23,13 @@ namespace {
 constexpr int kAhead = 3;       // token rows in flight per thread
 constexpr int kMaxGroups = 4;
 constexpr int kThreadsPerSM = 1024;
+constexpr int kMaxV = 4;                       // pieces of a thread
+constexpr int kMaxThreads = 512;                // 8192 channels, pieces of 4
+constexpr int kMaxWarps = kMaxThreads / 32;
 
 struct Shared {
   alignas(16) float2 cs[3][kMaxGroups][64];   // written one token ahead: three in turn
-  alignas(16) float red[2][kMaxGroups][2 * kMaxRowWarps];
+  alignas(16) float red[2][kMaxGroups][2 * kMaxWarps];
 };
 
 // The angles of a thread: pairs t and t + threads of the group.
@@ -73,55 +76,59 @@ struct Turner {
   }
 };
 
-// v = R u (kBack: R^T u) on four pairs.
-template <bool kBack>
-__device__ __forceinline__ void turn8(const float2* cs, float* v) {
+// v = R u (kBack: R^T u) on a thread's E/2 pairs.
+template <bool kBack, int E>
+__device__ __forceinline__ void turn_piece(const float2 (&cs)[E / 2], float* v) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < E / 2; ++i) {
     const float c = cs[i].x, s = kBack ? -cs[i].y : cs[i].y;
     const float a = v[2 * i], b = v[2 * i + 1];
     v[2 * i] = fmaf(a, c, -b * s);
     v[2 * i + 1] = fmaf(a, s, b * c);
   }
 }
-__device__ __forceinline__ void load_turns(const float2* p, float2* cs) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 2);
-  cs[0] = make_float2(a.x, a.y);
-  cs[1] = make_float2(a.z, a.w);
-  cs[2] = make_float2(b.x, b.y);
-  cs[3] = make_float2(b.z, b.w);
+template <int E>
+__device__ __forceinline__ void load_turns(const float2* p, float2 (&cs)[E / 2]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; i += 2) {
+    const float4 a = *reinterpret_cast<const float4*>(p + i);
+    cs[i] = make_float2(a.x, a.y);
+    cs[i + 1] = make_float2(a.z, a.w);
+  }
 }
 
-// Sum over the threads that hold one head's channels (d/8 neighbouring lanes: 8 or 16).
+// Sum over the threads that hold one head's channels (d/E neighbouring lanes: 8, 16 or 32).
+template <int E>
 __device__ __forceinline__ float head_sum(float v, int d) {
   v += __shfl_xor_sync(0xffffffffu, v, 1);
   v += __shfl_xor_sync(0xffffffffu, v, 2);
   v += __shfl_xor_sync(0xffffffffu, v, 4);
-  if (d == 128) v += __shfl_xor_sync(0xffffffffu, v, 8);
+  if (d > 8 * E) v += __shfl_xor_sync(0xffffffffu, v, 8);
+  if (d > 16 * E) v += __shfl_xor_sync(0xffffffffu, v, 16);
   return v;
 }
 
 // grid (token groups, B, q | k).
-template <typename T, int NORM, bool ROT, int V>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int W, const T* q,
+template <typename T, int E, int NORM, bool ROT, int V>
+__global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int W, const T* q,
                                                         const T* k, const float* __restrict__ wq,
                                                         const float* __restrict__ wk, T* qo, T* ko) {
-  constexpr int kPieces = V * Raw8<T>::kPieces;
+  constexpr int kRow = V * piece_bytes<E, T>();   // bytes of a row per thread
   __shared__ Shared sh;
-  extern __shared__ uint4 ring[];      // [kAhead][pieces][threads]
+  extern __shared__ __align__(16) uint8_t ring[];   // [kAhead][V][tensors][threads] pieces
   const RowGroup rg(W);
   const int G = blockDim.x / (32 * W), b = blockIdx.y, nt = blockDim.x;
   const bool is_k = blockIdx.z;
   const rola_strides si = is_k ? a.k : a.q, so = is_k ? a.ko : a.qo;
   const float* w = is_k ? wk : wq;
-  const int h0 = (kVec * rg.t) >> a.head_shift, c = (kVec * rg.t) & (a.d - 1), hs = (kVec * 32 * W) >> a.head_shift;
+  const int h0 = (E * rg.t) >> a.head_shift, c = (E * rg.t) & (a.d - 1), hs = (E * 32 * W) >> a.head_shift;
   const T* src = (is_k ? k : q) + b * si.b + h0 * si.h + c;
   T* dst = (is_k ? ko : qo) + b * so.b + h0 * so.h + c;
-  float gain[V][kVec];
+  float gain[V][E];
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < E; ++i) {
       const bool on = h0 + j * hs < a.H;
       gain[j][i] = NORM == ROLA_NORM_NONE || !on ? 1.f
                    : NORM == ROLA_NORM_HEAD      ? __ldg(w + c + i)
@@ -130,13 +137,12 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
   const Turner turner(a, rg.t, 32 * W);
   const float inv = 1.f / (NORM == ROLA_NORM_TOKEN ? a.H * a.d : a.d);
   const int first = blockIdx.x * G + rg.g, step = gridDim.x * G;
-  uint4* mine = ring + threadIdx.x;
   auto fetch = [&](long long n, int s) {
     if (n < a.N) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (h0 + j * hs < a.H)
-          copy_vec(mine + (s * kPieces + j * Raw8<T>::kPieces) * nt, nt, src + n * si.n + j * hs * si.h);
+          fetch_piece<E>(ring + (s * kRow + j * piece_bytes<E, T>()) * nt, src + n * si.n + j * hs * si.h);
     }
     copy_commit();
   };
@@ -147,21 +153,19 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
   for (long long n = first; n < a.N; n += step, ++it) {
     fetch(n + (long long)(kAhead - 1) * step, slot == 0 ? kAhead - 1 : slot - 1);
     copy_wait<kAhead - 1>();
-    float x[V][kVec];
+    float x[V][E];
     float sum = 0.f, rms[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const bool on = h0 + j * hs < a.H;
-      Raw8<T> raw;
-      raw.slot(mine + (slot * kPieces + j * Raw8<T>::kPieces) * nt, nt);
-      raw.get(x[j]);
+      read_piece<E, T>(ring + (slot * kRow + j * piece_bytes<E, T>()) * nt, x[j]);
       float s = 0.f;
       if (NORM != ROLA_NORM_NONE && on) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) s = fmaf(x[j][i], x[j][i], s);
+        for (int i = 0; i < E; ++i) s = fmaf(x[j][i], x[j][i], s);
       }
       sum += s;
-      if (NORM == ROLA_NORM_HEAD) rms[j] = rsqrtf(fmaf(head_sum(s, a.d), inv, a.eps));
+      if (NORM == ROLA_NORM_HEAD) rms[j] = rsqrtf(fmaf(head_sum<E>(s, a.d), inv, a.eps));
     }
     const int next = turn == 2 ? 0 : turn + 1;
     if (ROT && n + step < a.N) turner.write(a, b, (int)(n + step), sh.cs[next][rg.g]);
@@ -170,23 +174,23 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
       unit = rsqrtf(fmaf(group_sum(rg, sum, sh.red[it & 1][rg.g]), inv, a.eps));
     else if (ROT)
       rg.sync();
-    float2 cs[4];
+    float2 cs[E / 2];
     if (ROT) {
-      load_turns(sh.cs[turn][rg.g] + (c >> 1), cs);
+      load_turns<E>(sh.cs[turn][rg.g] + (c >> 1), cs);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) cs[i] = make_float2(cs[i].x * unit, cs[i].y * unit);
+      for (int i = 0; i < E / 2; ++i) cs[i] = make_float2(cs[i].x * unit, cs[i].y * unit);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (h0 + j * hs >= a.H) continue;
       const float f = (NORM == ROLA_NORM_HEAD ? rms[j] : 1.f) * (ROT ? 1.f : unit);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
+      for (int i = 0; i < E; ++i) {
         if (NORM != ROLA_NORM_NONE) x[j][i] *= gain[j][i];
         if (NORM == ROLA_NORM_HEAD || (NORM == ROLA_NORM_TOKEN && !ROT)) x[j][i] *= f;
       }
-      if (ROT) turn8<false>(cs, x[j]);
-      store8(dst + n * so.n + j * hs * so.h, x[j]);
+      if (ROT) turn_piece<false, E>(cs, x[j]);
+      store_piece<E>(dst + n * so.n + j * hs * so.h, x[j]);
     }
     slot = slot == kAhead - 1 ? 0 : slot + 1;
     turn = next;
@@ -195,29 +199,29 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
 }
 
 // Backward.  dq, dk are contiguous.  part: [gridDim.x * B * G][2][H * d] partial sums of dw.
-template <typename T, typename TG, int NORM, bool ROT, int V>
-__global__ void __launch_bounds__(256, V == 4 ? 1 : 2) norm_rope_backward_kernel(
+template <typename T, typename TG, int E, int NORM, bool ROT, int V>
+__global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward_kernel(
     const __grid_constant__ NormRopeArgs a, int W, const TG* dqo, const TG* dko, const T* __restrict__ q,
     const T* __restrict__ k, const float* __restrict__ wq, const float* __restrict__ wk, T* dq, T* dk,
     float* __restrict__ part) {
-  constexpr int kPg = Raw8<TG>::kPieces, kPx = NORM == ROLA_NORM_NONE ? 0 : Raw8<T>::kPieces;
-  constexpr int kPieces = V * (kPg + kPx);
+  constexpr int kBg = piece_bytes<E, TG>(), kBx = NORM == ROLA_NORM_NONE ? 0 : piece_bytes<E, T>();
+  constexpr int kRow = V * (kBg + kBx);            // bytes of a row per thread
   __shared__ Shared sh;
-  extern __shared__ uint4 ring[];      // [kAhead][pieces][threads]
+  extern __shared__ __align__(16) uint8_t ring[];   // [kAhead][V][tensors][threads] pieces
   const RowGroup rg(W);
   const int G = blockDim.x / (32 * W), b = blockIdx.y, nt = blockDim.x, C = a.H * a.d;
   const bool is_k = blockIdx.z;
   const rola_strides si = is_k ? a.k : a.q, su = is_k ? a.ko : a.qo;
   const float* w = is_k ? wk : wq;
-  const int h0 = (kVec * rg.t) >> a.head_shift, c = (kVec * rg.t) & (a.d - 1), hs = (kVec * 32 * W) >> a.head_shift;
+  const int h0 = (E * rg.t) >> a.head_shift, c = (E * rg.t) & (a.d - 1), hs = (E * 32 * W) >> a.head_shift;
   const T* src = NORM == ROLA_NORM_NONE ? nullptr : (is_k ? k : q) + b * si.b + h0 * si.h + c;
   const TG* up = (is_k ? dko : dqo) + b * su.b + h0 * su.h + c;
   T* dst = (is_k ? dk : dq) + ((size_t)b * a.N * a.H + h0) * a.d + c;
-  float gain[V][kVec], acc[V][kVec];
+  float gain[V][E], acc[V][E];
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < E; ++i) {
       const bool on = h0 + j * hs < a.H;
       gain[j][i] = NORM == ROLA_NORM_NONE || !on ? 0.f
                    : NORM == ROLA_NORM_HEAD      ? __ldg(w + c + i)
@@ -227,15 +231,14 @@ __global__ void __launch_bounds__(256, V == 4 ? 1 : 2) norm_rope_backward_kernel
   const Turner turner(a, rg.t, 32 * W);
   const float inv = 1.f / (NORM == ROLA_NORM_TOKEN ? C : a.d);
   const int first = blockIdx.x * G + rg.g, step = gridDim.x * G;
-  uint4* mine = ring + threadIdx.x;
   auto fetch = [&](long long n, int s) {
     if (n < a.N) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (h0 + j * hs < a.H) {
-          uint4* at = mine + (s * kPieces + j * (kPg + kPx)) * nt;
-          copy_vec(at, nt, up + n * su.n + j * hs * su.h);
-          if (NORM != ROLA_NORM_NONE) copy_vec(at + kPg * nt, nt, src + n * si.n + j * hs * si.h);
+          uint8_t* at = ring + (s * kRow + j * (kBg + kBx)) * nt;
+          fetch_piece<E>(at, up + n * su.n + j * hs * su.h);
+          if (NORM != ROLA_NORM_NONE) fetch_piece<E>(at + kBg * nt, src + n * si.n + j * hs * si.h);
         }
     }
     copy_commit();
@@ -248,27 +251,23 @@ __global__ void __launch_bounds__(256, V == 4 ? 1 : 2) norm_rope_backward_kernel
   for (long long n = first; n < a.N; n += step, ++it) {
     fetch(n + (long long)(kAhead - 1) * step, slot == 0 ? kAhead - 1 : slot - 1);
     copy_wait<kAhead - 1>();
-    float2 cs[4];
-    if (ROT) load_turns(sh.cs[turn][rg.g] + (c >> 1), cs);
-    float g[V][kVec];
+    float2 cs[E / 2];
+    if (ROT) load_turns<E>(sh.cs[turn][rg.g] + (c >> 1), cs);
+    float g[V][E];
     float s0 = 0.f, s1 = 0.f, r[V], m[V];   // sums of x^2 and of h x;  1/rms and r^2 mean(h x)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const bool on = h0 + j * hs < a.H;
-      const uint4* at = mine + (slot * kPieces + j * (kPg + kPx)) * nt;
-      Raw8<TG> raw;
-      raw.slot(at, nt);
-      raw.get(g[j]);
-      if (ROT) turn8<true>(cs, g[j]);
+      const uint8_t* at = ring + (slot * kRow + j * (kBg + kBx)) * nt;
+      read_piece<E, TG>(at, g[j]);
+      if (ROT) turn_piece<true, E>(cs, g[j]);
       if (NORM != ROLA_NORM_NONE) {
-        Raw8<T> raw_x;                 // read again below: cheaper than V x 8 more registers
-        float x[kVec];
-        raw_x.slot(at + kPg * nt, nt);
-        raw_x.get(x);
+        float x[E];                    // read again below: cheaper than V x E more registers
+        read_piece<E, T>(at + kBg * nt, x);
         float t0 = 0.f, t1 = 0.f;
         if (on) {
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) {
+          for (int i = 0; i < E; ++i) {
             t0 = fmaf(x[i], x[i], t0);
             t1 = fmaf(g[j][i] * gain[j][i], x[i], t1);
           }
@@ -276,8 +275,8 @@ __global__ void __launch_bounds__(256, V == 4 ? 1 : 2) norm_rope_backward_kernel
         s0 += t0;
         s1 += t1;
         if (NORM == ROLA_NORM_HEAD) {
-          r[j] = rsqrtf(fmaf(head_sum(t0, a.d), inv, a.eps));
-          m[j] = head_sum(t1, a.d) * inv * r[j] * r[j];
+          r[j] = rsqrtf(fmaf(head_sum<E>(t0, a.d), inv, a.eps));
+          m[j] = head_sum<E>(t1, a.d) * inv * r[j] * r[j];
         }
       }
     }
@@ -297,17 +296,15 @@ __global__ void __launch_bounds__(256, V == 4 ? 1 : 2) norm_rope_backward_kernel
     for (int j = 0; j < V; ++j) {
       if (h0 + j * hs >= a.H) continue;
       if (NORM != ROLA_NORM_NONE) {
-        Raw8<T> raw_x;
-        float x[kVec];
-        raw_x.slot(mine + (slot * kPieces + j * (kPg + kPx) + kPg) * nt, nt);
-        raw_x.get(x);
+        float x[E];
+        read_piece<E, T>(ring + (slot * kRow + j * (kBg + kBx) + kBg) * nt, x);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
+        for (int i = 0; i < E; ++i) {
           acc[j][i] = fmaf(g[j][i], x[i] * r[j], acc[j][i]);
           g[j][i] = r[j] * (g[j][i] * gain[j][i] - x[i] * m[j]);
         }
       }
-      store8(dst + ((size_t)n * a.H + j * hs) * a.d, g[j]);
+      store_piece<E>(dst + ((size_t)n * a.H + j * hs) * a.d, g[j]);
     }
     slot = slot == kAhead - 1 ? 0 : slot + 1;
     turn = next;
@@ -318,7 +315,7 @@ __global__ void __launch_bounds__(256, V == 4 ? 1 : 2) norm_rope_backward_kernel
     float* p = part + (group * 2 + is_k) * C + (size_t)h0 * a.d + c;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (h0 + j * hs < a.H) store8(p + (size_t)j * hs * a.d, acc[j]);
+      if (h0 + j * hs < a.H) store_floats<E>(p + (size_t)j * hs * a.d, acc[j]);
   }
 }
 
@@ -338,26 +335,30 @@ int token_blocks(const RowShape& s, int B, int N, int tensors) {
 
 template <typename K>
 cudaError_t opt_in(K kern, size_t smem) {
-  return smem <= 40 * 1024 ? cudaSuccess
+  return smem <= 40 * 1024 ? cudaSuccess   // with the static part within the default
                            : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
+
+// Channels of a piece.
+template <typename... Ts>
+constexpr int kE = (std::is_same_v<Ts, float> || ...) ? 4 : 8;
 
 template <typename T, int NORM, bool ROT, int V>
 cudaError_t forward_v(const NormRopeArgs& a, const RowShape& s, const void* q, const void* k, const float* wq,
                       const float* wk, void* qo, void* ko, cudaStream_t st) {
-  const size_t smem = 16 * (size_t)kAhead * V * Raw8<T>::kPieces * s.threads;
+  const size_t smem = (size_t)kAhead * V * piece_bytes<kE<T>, T>() * s.threads;
   const int tensors = k ? 2 : 1;
-  cudaError_t e = opt_in(norm_rope_kernel<T, NORM, ROT, V>, smem);
+  cudaError_t e = opt_in(norm_rope_kernel<T, kE<T>, NORM, ROT, V>, smem);
   if (e != cudaSuccess) return e;
-  norm_rope_kernel<T, NORM, ROT, V><<<dim3(token_blocks(s, a.B, a.N, tensors), a.B, tensors), s.threads, smem, st>>>(
-      a, s.W, (const T*)q, (const T*)k, wq, wk, (T*)qo, (T*)ko);
+  norm_rope_kernel<T, kE<T>, NORM, ROT, V>
+      <<<dim3(token_blocks(s, a.B, a.N, tensors), a.B, tensors), s.threads, smem, st>>>(a, s.W, (const T*)q, (const T*)k, wq, wk, (T*)qo, (T*)ko);
   return cudaGetLastError();
 }
 
 template <typename T, int NORM>
 cudaError_t forward(const NormRopeArgs& a, const void* q, const void* k, const float* wq, const float* wk, void* qo,
                     void* ko, cudaStream_t st) {
-  const RowShape s = row_shape(a.H * a.d, 4);
+  const RowShape s = row_shape(a.H * a.d, kE<T>, kMaxV, kMaxWarps);
   auto go = [&](auto rot) {
     constexpr bool R = decltype(rot)::value;
     return s.V == 1   ? forward_v<T, NORM, R, 1>(a, s, q, k, wq, wk, qo, ko, st)
@@ -371,11 +372,12 @@ template <typename T, typename TG, int NORM, bool ROT, int V>
 cudaError_t backward_v(const NormRopeArgs& a, const RowShape& s, const void* dqo, const void* dko, const void* q,
                        const void* k, const float* wq, const float* wk, void* dq, void* dk, float* dwq, float* dwk,
                        float* part, cudaStream_t st) {
-  const size_t smem = 16 * (size_t)kAhead * V * (Raw8<TG>::kPieces + (NORM ? Raw8<T>::kPieces : 0)) * s.threads;
+  constexpr int E = kE<T, TG>;
+  const size_t smem = (size_t)kAhead * V * (piece_bytes<E, TG>() + (NORM ? piece_bytes<E, T>() : 0)) * s.threads;
   const int tensors = dko ? 2 : 1, C = a.H * a.d, blocks = token_blocks(s, a.B, a.N, tensors);
-  cudaError_t e = opt_in(norm_rope_backward_kernel<T, TG, NORM, ROT, V>, smem);
+  cudaError_t e = opt_in(norm_rope_backward_kernel<T, TG, E, NORM, ROT, V>, smem);
   if (e != cudaSuccess) return e;
-  norm_rope_backward_kernel<T, TG, NORM, ROT, V><<<dim3(blocks, a.B, tensors), s.threads, smem, st>>>(
+  norm_rope_backward_kernel<T, TG, E, NORM, ROT, V><<<dim3(blocks, a.B, tensors), s.threads, smem, st>>>(
       a, s.W, (const TG*)dqo, (const TG*)dko, (const T*)q, (const T*)k, wq, wk, (T*)dq, (T*)dk, part);
   e = cudaGetLastError();
   if (e != cudaSuccess || NORM == ROLA_NORM_NONE) return e;
@@ -389,7 +391,7 @@ template <typename T, typename TG, int NORM>
 cudaError_t backward(const NormRopeArgs& a, const void* dqo, const void* dko, const void* q, const void* k,
                      const float* wq, const float* wk, void* dq, void* dk, float* dwq, float* dwk, float* part,
                      cudaStream_t st) {
-  const RowShape s = row_shape(a.H * a.d, 4);
+  const RowShape s = row_shape(a.H * a.d, kE<T, TG>, kMaxV, kMaxWarps);
   auto go = [&](auto rot) {
     constexpr bool R = decltype(rot)::value;
     return s.V == 1   ? backward_v<T, TG, NORM, R, 1>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st)
@@ -415,8 +417,13 @@ cudaError_t forward_norm(rola_qk_norm norm, const A&... x) {
 }  // namespace
 
 int norm_rope_parts(int B, int N, int C, int tensors) {
-  const RowShape s = row_shape(C, 4);
-  return token_blocks(s, B, N, tensors) * B * s.G;
+  int most = 0;
+  for (int e : {4, 8}) {               // for either type of piece
+    const RowShape s = row_shape(C, e, kMaxV, kMaxWarps);
+    const int n = token_blocks(s, B, N, tensors) * B * s.G;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, rola_dtype dt, rola_qk_norm norm, const void* q, const void* k,

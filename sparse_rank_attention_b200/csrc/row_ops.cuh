@@ -1,8 +1,8 @@
 // Building blocks of the kernels that work on whole token rows (norms, rotary positions).  A row
-// is owned by a group of W warps; thread t of the group holds V vectors of 8 channels of every
-// row it meets: t, t + 32 W, ...  Rows to come are fetched by asynchronous copies into slots of
-// shared memory that only the thread itself reads, so that fetching ahead costs neither registers
-// nor barriers.
+// is owned by a group of W warps; thread t of the group holds V pieces of E neighbouring channels
+// of every row it meets: pieces t, t + 32 W, ...  Rows to come are fetched by asynchronous copies
+// into slots of shared memory that only the thread itself reads, so that fetching ahead costs
+// neither registers nor barriers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -18,16 +18,16 @@ constexpr int kMaxRowChannels = 8192;
 constexpr int kMaxRowWarps = 8;      // of a group: 8192 channels at V = 4
 constexpr int kRowSMs = 148;
 
-// Threads of a row: W warps with V vectors each.  More vectors per thread mean fewer threads to
+// Threads of a row: W warps with V pieces each.  More pieces per thread mean fewer threads to
 // reduce over; among the V whose last warp is not much emptier, the largest is taken.
 struct RowShape {
   int V, W, G, threads;   // G groups in a block
 };
-inline RowShape row_shape(int C, int max_v, int max_warps = kMaxRowWarps) {
-  const int vecs = C / kVec;
-  RowShape s{1, (vecs + 31) / 32, 1, 0};
+inline RowShape row_shape(int C, int E, int max_v, int max_warps = kMaxRowWarps) {
+  const int pieces = C / E;
+  RowShape s{1, (pieces + 31) / 32, 1, 0};
   for (int v = 2; v <= max_v; v *= 2) {
-    const int w = (vecs + 32 * v - 1) / (32 * v);
+    const int w = (pieces + 32 * v - 1) / (32 * v);
     if (s.W > max_warps || 8ll * v * w <= 9ll * s.V * s.W) s.V = v, s.W = w;
   }
   s.G = s.W >= 4 ? 1 : 4 / s.W;
@@ -35,15 +35,16 @@ inline RowShape row_shape(int C, int max_v, int max_warps = kMaxRowWarps) {
   return s;
 }
 
-template <typename T>
-struct Raw8;
+// E neighbouring channels of type T, as a thread moves them: 16 bytes, or 8 where bf16 stands
+// beside fp32.  E is 8 where all tensors are bf16 and 4 where one is fp32, so that a warp's access
+// always covers whole 32-byte sectors (8 fp32 channels as two 16-byte halves would touch every
+// sector twice, and write each in two parts).
+template <typename T, int E>
+struct Piece;
 template <>
-struct Raw8<__nv_bfloat16> {
-  static constexpr int kPieces = 1;   // 16-byte pieces of a vector
-  uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void slot(const uint4* s, int) { a = *s; }
-  __device__ __forceinline__ void get(float* v) const {
+struct Piece<__nv_bfloat16, 8> {
+  using Raw = uint4;
+  static __device__ __forceinline__ void get(const uint4& a, float* v) {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -51,59 +52,88 @@ struct Raw8<__nv_bfloat16> {
       v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  // the one rounding of an output: round to nearest even
+  static __device__ __forceinline__ uint4 put(const float* v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
 template <>
-struct Raw8<float> {
-  static constexpr int kPieces = 2;
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
+struct Piece<__nv_bfloat16, 4> {
+  using Raw = uint2;
+  static __device__ __forceinline__ void get(const uint2& a, float* v) {
+    v[0] = __uint_as_float(a.x << 16);
+    v[1] = __uint_as_float(a.x & 0xffff0000u);
+    v[2] = __uint_as_float(a.y << 16);
+    v[3] = __uint_as_float(a.y & 0xffff0000u);
   }
-  __device__ __forceinline__ void slot(const uint4* s, int stride) {
-    a = *reinterpret_cast<const float4*>(s);
-    b = *reinterpret_cast<const float4*>(s + stride);
-  }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  static __device__ __forceinline__ uint2 put(const float* v) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]), g = __floats2bfloat162_rn(v[2], v[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&h), *reinterpret_cast<const uint32_t*>(&g));
   }
 };
-
-// The one rounding of an output (round to nearest even; fp32 is stored as it is).
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+template <>
+struct Piece<float, 4> {
+  using Raw = float4;
+  static __device__ __forceinline__ void get(const float4& a, float* v) {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  static __device__ __forceinline__ float4 put(const float* v) { return make_float4(v[0], v[1], v[2], v[3]); }
+};
+template <int E, typename T>
+__device__ __forceinline__ void load_piece(const T* p, float* v) {
+  Piece<T, E>::get(*reinterpret_cast<const typename Piece<T, E>::Raw*>(p), v);
 }
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+template <int E, typename T>
+__device__ __forceinline__ void store_piece(T* p, const float* v) {
+  *reinterpret_cast<typename Piece<T, E>::Raw*>(p) = Piece<T, E>::put(v);
 }
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  Raw8<float> r;
-  r.load(p);
-  r.get(v);
+template <int E, typename T>
+__host__ __device__ constexpr int piece_bytes() { return E * (int)sizeof(T); }
+// E fp32 values (gains, modulations, partial sums).
+template <int E>
+__device__ __forceinline__ void load_floats(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < E; i += 4) load_piece<4>(p + i, v + i);
 }
+template <int E>
+__device__ __forceinline__ void store_floats(float* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < E; i += 4) store_piece<4>(p + i, v + i);
+}
+// 8 channels of either type.
+__device__ __forceinline__ void load8(const float* p, float* v) { load_floats<8>(p, v); }
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) { load_piece<8>(p, v); }
+__device__ __forceinline__ void store8(float* p, const float* v) { store_floats<8>(p, v); }
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) { store_piece<8>(p, v); }
 
-// Asynchronous 16-byte copies, waited for in groups: `keep` groups may still be in flight.
-__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_addr(dst)), "l"(src) : "memory");
+// Asynchronous copies into shared memory, waited for in groups: `keep` may still be in flight.
+template <int bytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  if constexpr (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_addr(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(sm100::smem_addr(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int keep>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(keep) : "memory");
 }
-// A vector of T into the thread's slot (pieces `stride` slots apart).
-template <typename T>
-__device__ __forceinline__ void copy_vec(uint4* slot, int stride, const T* src) {
-#pragma unroll
-  for (int p = 0; p < Raw8<T>::kPieces; ++p) copy16(slot + p * stride, reinterpret_cast<const uint4*>(src) + p);
+// A piece of T into the thread's slot of a plane [threads], and out of it.
+template <int E, typename T>
+__device__ __forceinline__ void fetch_piece(uint8_t* plane, const T* src) {
+  constexpr int n = piece_bytes<E, T>();
+  copy_async<n>(plane + threadIdx.x * n, src);
+}
+template <int E, typename T>
+__device__ __forceinline__ void read_piece(const uint8_t* plane, float* v) {
+  Piece<T, E>::get(reinterpret_cast<const typename Piece<T, E>::Raw*>(plane)[threadIdx.x], v);
 }
 
 // A thread's place in its group.
