@@ -8,9 +8,10 @@
 // registers between the statistics and the rotation.  A group of warps owns the rows of one
 // tensor (q or k); a thread has up to four pieces of E channels, at the same channels of their
 // heads (a group's width is a multiple of the head), so that one set of E/2 angles serves them
-// all and 1/rms is folded into it.  A token's d/2 angles are formed one token ahead by the first
-// threads of the group: the angle in fp64 turns, reduced to one turn (exact to 2^-53 of the
-// position), then sincospi in fp32.
+// all and 1/rms is folded into it.  Angles are formed in fp64 turns, reduced to one turn (exact to
+// 2^-53 of the position), then sincospi in fp32: for a grid whose axes fit, once per block into a
+// table in shared memory (t + h + w positions instead of t * h * w); else per token, one token
+// ahead, by the first threads of the group.
 #include <cmath>
 #include <type_traits>
 
@@ -31,6 +32,70 @@ struct Shared {
   alignas(16) float2 cs[3][kMaxGroups][64];   // written one token ahead: three in turn
   alignas(16) float red[2][kMaxGroups][2 * kMaxWarps];
 };
+
+// cos and sin of an angle given in turns.
+__device__ __forceinline__ float2 cos_sin(double turn) {
+  turn -= rint(turn);
+  float2 v;
+  sincospif(2.f * (float)turn, &v.y, &v.x);
+  return v;
+}
+
+constexpr int kTableMost = 4096;   // entries: 32 KB
+__host__ __device__ inline long long table_entries(const NormRopeArgs& a) {
+  const RotArgs& r = a.rot;
+  return (long long)r.gt * r.pt + (long long)r.gh * r.ph + (long long)r.gw * (a.d / 2 - r.pt - r.ph);
+}
+
+// The table of a grid's angles: axis by axis, [position][pair of the axis].
+__device__ __forceinline__ void write_table(const NormRopeArgs& a, float2* tab) {
+  const RotArgs& r = a.rot;
+  const int pw = a.d / 2 - r.pt - r.ph;
+  const int n[3] = {r.gt, r.gh, r.gw}, c[3] = {r.pt, r.ph, pw}, s[3] = {r.st, r.sh, r.sw};
+  for (int axis = 0, first = 0; axis < 3; ++axis) {
+    for (int e = threadIdx.x; e < n[axis] * c[axis]; e += blockDim.x) {
+      const int p = e / c[axis], i = e - p * c[axis];
+      tab[e] = cos_sin((double)((long long)p + s[axis]) * r.turns[first + i]);
+    }
+    tab += n[axis] * c[axis];
+    first += c[axis];
+  }
+}
+
+// A thread's walk over that table: tokens n, n + step, ... of the grid, E/2 pairs from pair c on.
+template <int E>
+struct Walker {
+  int t, y, x, dt, dy, dx;
+  int axis[E / 2], at[E / 2];
+  __device__ __forceinline__ Walker(const NormRopeArgs& a, int c, int n, int step) {
+    const RotArgs& r = a.rot;
+    const int hw = r.gh * r.gw;
+    t = n / hw, y = n % hw / r.gw, x = n % r.gw;
+    dt = step / hw, dy = step % hw / r.gw, dx = step % r.gw;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const int p = c + i;
+      axis[i] = p < r.pt ? 0 : p < r.pt + r.ph ? 1 : 2;
+      at[i] = axis[i] == 0 ? p : axis[i] == 1 ? r.gt * r.pt + p - r.pt : r.gt * r.pt + r.gh * r.ph + p - r.pt - r.ph;
+    }
+  }
+  __device__ __forceinline__ void load(const NormRopeArgs& a, const float2* tab, float2 (&cs)[E / 2]) const {
+    const RotArgs& r = a.rot;
+    const int rt = t * r.pt, ry = y * r.ph, rx = x * (a.d / 2 - r.pt - r.ph);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)   // past the grid: not turned
+      cs[i] = t < r.gt ? tab[at[i] + (axis[i] == 0 ? rt : axis[i] == 1 ? ry : rx)] : make_float2(1.f, 0.f);
+  }
+  __device__ __forceinline__ void next(const NormRopeArgs& a) {
+    x += dx;
+    y += dy;
+    t += dt;
+    if (x >= a.rot.gw) x -= a.rot.gw, ++y;
+    if (y >= a.rot.gh) y -= a.rot.gh, ++t;
+  }
+};
+
+enum Rot { kNoRot = 0, kPerToken = 1, kTable = 2 };
 
 // The angles of a thread: pairs t and t + threads of the group.
 struct Turner {
@@ -67,25 +132,40 @@ struct Turner {
         p = 0;                         // past the grid: not turned
       else
         p = axis[i] == 0 ? (long long)tt + r.st : axis[i] == 1 ? (long long)y + r.sh : (long long)x + r.sw;
-      double turn = (double)p * turns[i];
-      turn -= rint(turn);
-      float2 v;
-      sincospif(2.f * (float)turn, &v.y, &v.x);
-      cs[pair[i]] = v;
+      cs[pair[i]] = cos_sin((double)p * turns[i]);
     }
   }
 };
 
-// v = R u (kBack: R^T u) on a thread's E/2 pairs.
+// v = R u (kBack: R^T u) on a thread's E/2 pairs: (a, b) -> a (c, s) + b (-s, c).
 template <bool kBack, int E>
 __device__ __forceinline__ void turn_piece(const float2 (&cs)[E / 2], float* v) {
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) {
     const float c = cs[i].x, s = kBack ? -cs[i].y : cs[i].y;
     const float a = v[2 * i], b = v[2 * i + 1];
-    v[2 * i] = fmaf(a, c, -b * s);
-    v[2 * i + 1] = fmaf(a, s, b * c);
+    float x = b, y = b;
+    sm100::mul2(x, y, -s, c);
+    sm100::fma2(v[2 * i], v[2 * i + 1], a, a, c, s, x, y);
   }
+}
+// d += a * b and d *= a on E values, two per instruction.
+template <int E>
+__device__ __forceinline__ void fma_piece(float* d, const float* a, const float* b) {
+#pragma unroll
+  for (int i = 0; i < E; i += 2) sm100::fma2(d[i], d[i + 1], a[i], a[i + 1], b[i], b[i + 1], d[i], d[i + 1]);
+}
+template <int E>
+__device__ __forceinline__ void mul_piece(float* d, const float* a) {
+#pragma unroll
+  for (int i = 0; i < E; i += 2) sm100::mul2(d[i], d[i + 1], a[i], a[i + 1]);
+}
+template <int E>
+__device__ __forceinline__ float dot_piece(const float* a, const float* b) {
+  float x = 0.f, y = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; i += 2) sm100::fma2(x, y, a[i], a[i + 1], b[i], b[i + 1], x, y);
+  return x + y;
 }
 template <int E>
 __device__ __forceinline__ void load_turns(const float2* p, float2 (&cs)[E / 2]) {
@@ -109,7 +189,7 @@ __device__ __forceinline__ float head_sum(float v, int d) {
 }
 
 // grid (token groups, B, q | k).
-template <typename T, int E, int NORM, bool ROT, int V>
+template <typename T, int E, int NORM, int ROT, int V>
 __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int W, const T* q,
                                                         const T* k, const float* __restrict__ wq,
                                                         const float* __restrict__ wk, T* qo, T* ko) {
@@ -124,6 +204,7 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
   const int h0 = (E * rg.t) >> a.head_shift, c = (E * rg.t) & (a.d - 1), hs = (E * 32 * W) >> a.head_shift;
   const T* src = (is_k ? k : q) + b * si.b + h0 * si.h + c;
   T* dst = (is_k ? ko : qo) + b * so.b + h0 * so.h + c;
+  const int64_t hx = hs * si.h, ho = hs * so.h;
   float gain[V][E];
 #pragma unroll
   for (int j = 0; j < V; ++j)
@@ -134,7 +215,8 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
                    : NORM == ROLA_NORM_HEAD      ? __ldg(w + c + i)
                                                  : __ldg(w + (size_t)(h0 + j * hs) * a.d + c + i);
     }
-  const Turner turner(a, rg.t, 32 * W);
+  const Turner turner(a, ROT == kPerToken ? rg.t : a.d, 32 * W);
+  float2* tab = reinterpret_cast<float2*>(ring + kAhead * kRow * nt);
   const float inv = 1.f / (NORM == ROLA_NORM_TOKEN ? a.H * a.d : a.d);
   const int first = blockIdx.x * G + rg.g, step = gridDim.x * G;
   auto fetch = [&](long long n, int s) {
@@ -142,13 +224,18 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (h0 + j * hs < a.H)
-          fetch_piece<E>(ring + (s * kRow + j * piece_bytes<E, T>()) * nt, src + n * si.n + j * hs * si.h);
+          fetch_piece<E>(ring + (s * kRow + j * piece_bytes<E, T>()) * nt, src + n * si.n + j * hx);
     }
     copy_commit();
   };
 #pragma unroll
   for (int s = 0; s < kAhead - 1; ++s) fetch(first + (long long)s * step, s);
-  if (ROT && first < a.N) turner.write(a, b, first, sh.cs[0][rg.g]);
+  if (ROT == kPerToken && first < a.N) turner.write(a, b, first, sh.cs[0][rg.g]);
+  Walker<E> walk(a, c >> 1, first, step);
+  if (ROT == kTable) {
+    write_table(a, tab);
+    __syncthreads();
+  }
   int slot = 0, turn = 0, it = 0;
   for (long long n = first; n < a.N; n += step, ++it) {
     fetch(n + (long long)(kAhead - 1) * step, slot == 0 ? kAhead - 1 : slot - 1);
@@ -159,24 +246,25 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
     for (int j = 0; j < V; ++j) {
       const bool on = h0 + j * hs < a.H;
       read_piece<E, T>(ring + (slot * kRow + j * piece_bytes<E, T>()) * nt, x[j]);
-      float s = 0.f;
-      if (NORM != ROLA_NORM_NONE && on) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) s = fmaf(x[j][i], x[j][i], s);
-      }
+      const float s = NORM != ROLA_NORM_NONE && on ? dot_piece<E>(x[j], x[j]) : 0.f;
       sum += s;
       if (NORM == ROLA_NORM_HEAD) rms[j] = rsqrtf(fmaf(head_sum<E>(s, a.d), inv, a.eps));
     }
     const int next = turn == 2 ? 0 : turn + 1;
-    if (ROT && n + step < a.N) turner.write(a, b, (int)(n + step), sh.cs[next][rg.g]);
+    if (ROT == kPerToken && n + step < a.N) turner.write(a, b, (int)(n + step), sh.cs[next][rg.g]);
     float unit = 1.f;
     if (NORM == ROLA_NORM_TOKEN)
       unit = rsqrtf(fmaf(group_sum(rg, sum, sh.red[it & 1][rg.g]), inv, a.eps));
-    else if (ROT)
+    else if (ROT == kPerToken)
       rg.sync();
     float2 cs[E / 2];
     if (ROT) {
-      load_turns<E>(sh.cs[turn][rg.g] + (c >> 1), cs);
+      if (ROT == kTable) {
+        walk.load(a, tab, cs);
+        walk.next(a);
+      } else {
+        load_turns<E>(sh.cs[turn][rg.g] + (c >> 1), cs);
+      }
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) cs[i] = make_float2(cs[i].x * unit, cs[i].y * unit);
     }
@@ -184,13 +272,13 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
     for (int j = 0; j < V; ++j) {
       if (h0 + j * hs >= a.H) continue;
       const float f = (NORM == ROLA_NORM_HEAD ? rms[j] : 1.f) * (ROT ? 1.f : unit);
+      if (NORM != ROLA_NORM_NONE) mul_piece<E>(x[j], gain[j]);
+      if (NORM == ROLA_NORM_HEAD || (NORM == ROLA_NORM_TOKEN && !ROT)) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (NORM != ROLA_NORM_NONE) x[j][i] *= gain[j][i];
-        if (NORM == ROLA_NORM_HEAD || (NORM == ROLA_NORM_TOKEN && !ROT)) x[j][i] *= f;
+        for (int i = 0; i < E; ++i) x[j][i] *= f;
       }
       if (ROT) turn_piece<false, E>(cs, x[j]);
-      store_piece<E>(dst + n * so.n + j * hs * so.h, x[j]);
+      store_piece<E>(dst + n * so.n + j * ho, x[j]);
     }
     slot = slot == kAhead - 1 ? 0 : slot + 1;
     turn = next;
@@ -199,7 +287,7 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
 }
 
 // Backward.  dq, dk are contiguous.  part: [gridDim.x * B * G][2][H * d] partial sums of dw.
-template <typename T, typename TG, int E, int NORM, bool ROT, int V>
+template <typename T, typename TG, int E, int NORM, int ROT, int V>
 __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward_kernel(
     const __grid_constant__ NormRopeArgs a, int W, const TG* dqo, const TG* dko, const T* __restrict__ q,
     const T* __restrict__ k, const float* __restrict__ wq, const float* __restrict__ wk, T* dq, T* dk,
@@ -216,6 +304,7 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward
   const int h0 = (E * rg.t) >> a.head_shift, c = (E * rg.t) & (a.d - 1), hs = (E * 32 * W) >> a.head_shift;
   const T* src = NORM == ROLA_NORM_NONE ? nullptr : (is_k ? k : q) + b * si.b + h0 * si.h + c;
   const TG* up = (is_k ? dko : dqo) + b * su.b + h0 * su.h + c;
+  const int64_t hx = hs * si.h, hu = hs * su.h;
   T* dst = (is_k ? dk : dq) + ((size_t)b * a.N * a.H + h0) * a.d + c;
   float gain[V][E], acc[V][E];
 #pragma unroll
@@ -228,7 +317,8 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward
                                                  : __ldg(w + (size_t)(h0 + j * hs) * a.d + c + i);
       acc[j][i] = 0.f;
     }
-  const Turner turner(a, rg.t, 32 * W);
+  const Turner turner(a, ROT == kPerToken ? rg.t : a.d, 32 * W);
+  float2* tab = reinterpret_cast<float2*>(ring + kAhead * kRow * nt);
   const float inv = 1.f / (NORM == ROLA_NORM_TOKEN ? C : a.d);
   const int first = blockIdx.x * G + rg.g, step = gridDim.x * G;
   auto fetch = [&](long long n, int s) {
@@ -237,24 +327,34 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward
       for (int j = 0; j < V; ++j)
         if (h0 + j * hs < a.H) {
           uint8_t* at = ring + (s * kRow + j * (kBg + kBx)) * nt;
-          fetch_piece<E>(at, up + n * su.n + j * hs * su.h);
-          if (NORM != ROLA_NORM_NONE) fetch_piece<E>(at + kBg * nt, src + n * si.n + j * hs * si.h);
+          fetch_piece<E>(at, up + n * su.n + j * hu);
+          if (NORM != ROLA_NORM_NONE) fetch_piece<E>(at + kBg * nt, src + n * si.n + j * hx);
         }
     }
     copy_commit();
   };
 #pragma unroll
   for (int s = 0; s < kAhead - 1; ++s) fetch(first + (long long)s * step, s);
-  if (ROT && first < a.N) turner.write(a, b, first, sh.cs[0][rg.g]);
-  if (ROT) rg.sync();
+  if (ROT == kPerToken && first < a.N) turner.write(a, b, first, sh.cs[0][rg.g]);
+  Walker<E> walk(a, c >> 1, first, step);
+  if (ROT == kTable) {
+    write_table(a, tab);
+    __syncthreads();
+  }
+  if (ROT == kPerToken) rg.sync();
   int slot = 0, turn = 0, it = 0;
   for (long long n = first; n < a.N; n += step, ++it) {
     fetch(n + (long long)(kAhead - 1) * step, slot == 0 ? kAhead - 1 : slot - 1);
     copy_wait<kAhead - 1>();
     float2 cs[E / 2];
-    if (ROT) load_turns<E>(sh.cs[turn][rg.g] + (c >> 1), cs);
+    if (ROT == kTable) {
+      walk.load(a, tab, cs);
+      walk.next(a);
+    } else if (ROT) {
+      load_turns<E>(sh.cs[turn][rg.g] + (c >> 1), cs);
+    }
     float g[V][E];
-    float s0 = 0.f, s1 = 0.f, r[V], m[V];   // sums of x^2 and of h x;  1/rms and r^2 mean(h x)
+    float s0 = 0.f, s1 = 0.f, r[V], m[V];   // sums of x^2 and of h x;  r = 1/rms, m = mean(h x r)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const bool on = h0 + j * hs < a.H;
@@ -264,32 +364,30 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward
       if (NORM != ROLA_NORM_NONE) {
         float x[E];                    // read again below: cheaper than V x E more registers
         read_piece<E, T>(at + kBg * nt, x);
-        float t0 = 0.f, t1 = 0.f;
-        if (on) {
+        const float t0 = on ? dot_piece<E>(x, x) : 0.f;
+        float h[E];
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
-            t0 = fmaf(x[i], x[i], t0);
-            t1 = fmaf(g[j][i] * gain[j][i], x[i], t1);
-          }
-        }
+        for (int i = 0; i < E; ++i) h[i] = g[j][i];
+        mul_piece<E>(h, gain[j]);
+        const float t1 = on ? dot_piece<E>(h, x) : 0.f;
         s0 += t0;
         s1 += t1;
         if (NORM == ROLA_NORM_HEAD) {
           r[j] = rsqrtf(fmaf(head_sum<E>(t0, a.d), inv, a.eps));
-          m[j] = head_sum<E>(t1, a.d) * inv * r[j] * r[j];
+          m[j] = head_sum<E>(t1, a.d) * inv * r[j];
         }
       }
     }
     const int next = turn == 2 ? 0 : turn + 1;
-    if (ROT && n + step < a.N) turner.write(a, b, (int)(n + step), sh.cs[next][rg.g]);
+    if (ROT == kPerToken && n + step < a.N) turner.write(a, b, (int)(n + step), sh.cs[next][rg.g]);
     if (NORM == ROLA_NORM_TOKEN) {
       const float2 s = group_sum(rg, s0, s1, sh.red[it & 1][rg.g]);
-      if (ROT && W == 1) __syncwarp();
+      if (ROT == kPerToken && W == 1) __syncwarp();
       r[0] = rsqrtf(fmaf(s.x, inv, a.eps));
-      m[0] = s.y * inv * r[0] * r[0];
+      m[0] = s.y * inv * r[0];
 #pragma unroll
       for (int j = 1; j < V; ++j) r[j] = r[0], m[j] = m[0];
-    } else if (ROT) {
+    } else if (ROT == kPerToken) {
       rg.sync();
     }
 #pragma unroll
@@ -299,9 +397,13 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward
         float x[E];
         read_piece<E, T>(ring + (slot * kRow + j * (kBg + kBx) + kBg) * nt, x);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          acc[j][i] = fmaf(g[j][i], x[i] * r[j], acc[j][i]);
-          g[j][i] = r[j] * (g[j][i] * gain[j][i] - x[i] * m[j]);
+        for (int i = 0; i < E; i += 2) sm100::mul2(x[i], x[i + 1], r[j], r[j]);   // x / rms
+        fma_piece<E>(acc[j], g[j], x);
+        mul_piece<E>(g[j], gain[j]);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          sm100::fma2(g[j][i], g[j][i + 1], x[i], x[i + 1], -m[j], -m[j], g[j][i], g[j][i + 1]);
+          sm100::mul2(g[j][i], g[j][i + 1], r[j], r[j]);
         }
       }
       store_piece<E>(dst + ((size_t)n * a.H + j * hs) * a.d, g[j]);
@@ -339,14 +441,22 @@ cudaError_t opt_in(K kern, size_t smem) {
                            : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
+// The table pays where the blocks' copies of it hold fewer angles than their tokens.
+bool use_table(const NormRopeArgs& a, const RowShape& s, int tensors) {
+  if (a.rot.pos != ROLA_POS_GRID) return false;
+  const long long n = table_entries(a);
+  return n <= kTableMost && n * token_blocks(s, a.B, a.N, tensors) * 2 <= (long long)a.N * (a.d / 2);
+}
+
 // Channels of a piece.
 template <typename... Ts>
 constexpr int kE = (std::is_same_v<Ts, float> || ...) ? 4 : 8;
 
-template <typename T, int NORM, bool ROT, int V>
+template <typename T, int NORM, int ROT, int V>
 cudaError_t forward_v(const NormRopeArgs& a, const RowShape& s, const void* q, const void* k, const float* wq,
                       const float* wk, void* qo, void* ko, cudaStream_t st) {
-  const size_t smem = (size_t)kAhead * V * piece_bytes<kE<T>, T>() * s.threads;
+  const size_t smem = (size_t)kAhead * V * piece_bytes<kE<T>, T>() * s.threads +
+                      (ROT == kTable ? sizeof(float2) * table_entries(a) : 0);
   const int tensors = k ? 2 : 1;
   cudaError_t e = opt_in(norm_rope_kernel<T, kE<T>, NORM, ROT, V>, smem);
   if (e != cudaSuccess) return e;
@@ -360,20 +470,22 @@ cudaError_t forward(const NormRopeArgs& a, const void* q, const void* k, const f
                     void* ko, cudaStream_t st) {
   const RowShape s = row_shape(a.H * a.d, kE<T>, kMaxV, kMaxWarps);
   auto go = [&](auto rot) {
-    constexpr bool R = decltype(rot)::value;
+    constexpr int R = decltype(rot)::value;
     return s.V == 1   ? forward_v<T, NORM, R, 1>(a, s, q, k, wq, wk, qo, ko, st)
            : s.V == 2 ? forward_v<T, NORM, R, 2>(a, s, q, k, wq, wk, qo, ko, st)
                       : forward_v<T, NORM, R, 4>(a, s, q, k, wq, wk, qo, ko, st);
   };
-  return a.rot.pos == ROLA_POS_NONE ? go(std::false_type{}) : go(std::true_type{});
+  if (a.rot.pos == ROLA_POS_NONE) return go(std::integral_constant<int, kNoRot>{});
+  return use_table(a, s, k ? 2 : 1) ? go(std::integral_constant<int, kTable>{}) : go(std::integral_constant<int, kPerToken>{});
 }
 
-template <typename T, typename TG, int NORM, bool ROT, int V>
+template <typename T, typename TG, int NORM, int ROT, int V>
 cudaError_t backward_v(const NormRopeArgs& a, const RowShape& s, const void* dqo, const void* dko, const void* q,
                        const void* k, const float* wq, const float* wk, void* dq, void* dk, float* dwq, float* dwk,
                        float* part, cudaStream_t st) {
   constexpr int E = kE<T, TG>;
-  const size_t smem = (size_t)kAhead * V * (piece_bytes<E, TG>() + (NORM ? piece_bytes<E, T>() : 0)) * s.threads;
+  const size_t smem = (size_t)kAhead * V * (piece_bytes<E, TG>() + (NORM ? piece_bytes<E, T>() : 0)) * s.threads +
+                      (ROT == kTable ? sizeof(float2) * table_entries(a) : 0);
   const int tensors = dko ? 2 : 1, C = a.H * a.d, blocks = token_blocks(s, a.B, a.N, tensors);
   cudaError_t e = opt_in(norm_rope_backward_kernel<T, TG, E, NORM, ROT, V>, smem);
   if (e != cudaSuccess) return e;
@@ -393,12 +505,13 @@ cudaError_t backward(const NormRopeArgs& a, const void* dqo, const void* dko, co
                      cudaStream_t st) {
   const RowShape s = row_shape(a.H * a.d, kE<T, TG>, kMaxV, kMaxWarps);
   auto go = [&](auto rot) {
-    constexpr bool R = decltype(rot)::value;
+    constexpr int R = decltype(rot)::value;
     return s.V == 1   ? backward_v<T, TG, NORM, R, 1>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st)
            : s.V == 2 ? backward_v<T, TG, NORM, R, 2>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st)
                       : backward_v<T, TG, NORM, R, 4>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st);
   };
-  return a.rot.pos == ROLA_POS_NONE ? go(std::false_type{}) : go(std::true_type{});
+  if (a.rot.pos == ROLA_POS_NONE) return go(std::integral_constant<int, kNoRot>{});
+  return use_table(a, s, dko ? 2 : 1) ? go(std::integral_constant<int, kTable>{}) : go(std::integral_constant<int, kPerToken>{});
 }
 
 template <typename T, typename TG, typename... A>
