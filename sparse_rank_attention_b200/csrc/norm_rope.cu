@@ -137,35 +137,36 @@ struct Turner {
   }
 };
 
-// v = R u (kBack: R^T u) on a thread's E/2 pairs: (a, b) -> a (c, s) + b (-s, c).
-template <bool kBack, int E>
-__device__ __forceinline__ void turn_piece(const float2 (&cs)[E / 2], float* v) {
+// A piece as E/2 rotary pairs, two fp32 lanes to an instruction.
+template <typename T, int E>
+__device__ __forceinline__ void read_pairs(const uint8_t* plane, float2 (&v)[E / 2]) {
+  float f[E];
+  read_piece<E, T>(plane, f);
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
+  for (int i = 0; i < E / 2; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+template <int E, typename T>
+__device__ __forceinline__ void store_pairs(T* p, const float2 (&v)[E / 2]) {
+  float f[E];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) f[2 * i] = v[i].x, f[2 * i + 1] = v[i].y;
+  store_piece<E>(p, f);
+}
+// v = R u (kBack: R^T u).
+template <bool kBack, int P>
+__device__ __forceinline__ void rotate(const float2 (&cs)[P], float2 (&v)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
     const float c = cs[i].x, s = kBack ? -cs[i].y : cs[i].y;
-    const float a = v[2 * i], b = v[2 * i + 1];
-    float x = b, y = b;
-    sm100::mul2(x, y, -s, c);
-    sm100::fma2(v[2 * i], v[2 * i + 1], a, a, c, s, x, y);
+    v[i] = make_float2(fmaf(v[i].x, c, -v[i].y * s), fmaf(v[i].x, s, v[i].y * c));
   }
 }
-// d += a * b and d *= a on E values, two per instruction.
-template <int E>
-__device__ __forceinline__ void fma_piece(float* d, const float* a, const float* b) {
+template <int P>
+__device__ __forceinline__ float dot(const float2 (&a)[P], const float2 (&b)[P]) {
+  float2 s = __fmul2_rn(a[0], b[0]);
 #pragma unroll
-  for (int i = 0; i < E; i += 2) sm100::fma2(d[i], d[i + 1], a[i], a[i + 1], b[i], b[i + 1], d[i], d[i + 1]);
-}
-template <int E>
-__device__ __forceinline__ void mul_piece(float* d, const float* a) {
-#pragma unroll
-  for (int i = 0; i < E; i += 2) sm100::mul2(d[i], d[i + 1], a[i], a[i + 1]);
-}
-template <int E>
-__device__ __forceinline__ float dot_piece(const float* a, const float* b) {
-  float x = 0.f, y = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; i += 2) sm100::fma2(x, y, a[i], a[i + 1], b[i], b[i + 1], x, y);
-  return x + y;
+  for (int i = 1; i < P; ++i) s = __ffma2_rn(a[i], b[i], s);
+  return s.x + s.y;
 }
 template <int E>
 __device__ __forceinline__ void load_turns(const float2* p, float2 (&cs)[E / 2]) {
@@ -188,11 +189,22 @@ __device__ __forceinline__ float head_sum(float v, int d) {
   return v;
 }
 
+// The gains of channels c .. c + E - 1 of head h (1 where there are none).
+template <int NORM, int P>
+__device__ __forceinline__ void load_gain(const NormRopeArgs& a, const float* __restrict__ w, int h, int c,
+                                          float2 (&gain)[P]) {
+  const float* p = NORM == ROLA_NORM_HEAD ? w + c : w + (size_t)h * a.d + c;
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    gain[i] = NORM != ROLA_NORM_NONE && h < a.H ? __ldg(reinterpret_cast<const float2*>(p) + i) : make_float2(1.f, 1.f);
+}
+
 // grid (token groups, B, q | k).
 template <typename T, int E, int NORM, int ROT, int V>
 __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int W, const T* q,
                                                         const T* k, const float* __restrict__ wq,
                                                         const float* __restrict__ wk, T* qo, T* ko) {
+  constexpr int P = E / 2;
   constexpr int kRow = V * piece_bytes<E, T>();   // bytes of a row per thread
   __shared__ Shared sh;
   extern __shared__ __align__(16) uint8_t ring[];   // [kAhead][V][tensors][threads] pieces
@@ -205,16 +217,9 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
   const T* src = (is_k ? k : q) + b * si.b + h0 * si.h + c;
   T* dst = (is_k ? ko : qo) + b * so.b + h0 * so.h + c;
   const int64_t hx = hs * si.h, ho = hs * so.h;
-  float gain[V][E];
+  float2 gain[V][P];
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const bool on = h0 + j * hs < a.H;
-      gain[j][i] = NORM == ROLA_NORM_NONE || !on ? 1.f
-                   : NORM == ROLA_NORM_HEAD      ? __ldg(w + c + i)
-                                                 : __ldg(w + (size_t)(h0 + j * hs) * a.d + c + i);
-    }
+  for (int j = 0; j < V; ++j) load_gain<NORM>(a, w, h0 + j * hs, c, gain[j]);
   const Turner turner(a, ROT == kPerToken ? rg.t : a.d, 32 * W);
   float2* tab = reinterpret_cast<float2*>(ring + kAhead * kRow * nt);
   const float inv = 1.f / (NORM == ROLA_NORM_TOKEN ? a.H * a.d : a.d);
@@ -240,13 +245,13 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
   for (long long n = first; n < a.N; n += step, ++it) {
     fetch(n + (long long)(kAhead - 1) * step, slot == 0 ? kAhead - 1 : slot - 1);
     copy_wait<kAhead - 1>();
-    float x[V][E];
+    float2 x[V][P];
     float sum = 0.f, rms[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const bool on = h0 + j * hs < a.H;
-      read_piece<E, T>(ring + (slot * kRow + j * piece_bytes<E, T>()) * nt, x[j]);
-      const float s = NORM != ROLA_NORM_NONE && on ? dot_piece<E>(x[j], x[j]) : 0.f;
+      read_pairs<T, E>(ring + (slot * kRow + j * piece_bytes<E, T>()) * nt, x[j]);
+      const float s = NORM != ROLA_NORM_NONE && on ? dot(x[j], x[j]) : 0.f;
       sum += s;
       if (NORM == ROLA_NORM_HEAD) rms[j] = rsqrtf(fmaf(head_sum<E>(s, a.d), inv, a.eps));
     }
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
       unit = rsqrtf(fmaf(group_sum(rg, sum, sh.red[it & 1][rg.g]), inv, a.eps));
     else if (ROT == kPerToken)
       rg.sync();
-    float2 cs[E / 2];
+    float2 cs[P];
     if (ROT) {
       if (ROT == kTable) {
         walk.load(a, tab, cs);
@@ -266,19 +271,19 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
         load_turns<E>(sh.cs[turn][rg.g] + (c >> 1), cs);
       }
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) cs[i] = make_float2(cs[i].x * unit, cs[i].y * unit);
+      for (int i = 0; i < P; ++i) cs[i] = make_float2(cs[i].x * unit, cs[i].y * unit);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (h0 + j * hs >= a.H) continue;
       const float f = (NORM == ROLA_NORM_HEAD ? rms[j] : 1.f) * (ROT ? 1.f : unit);
-      if (NORM != ROLA_NORM_NONE) mul_piece<E>(x[j], gain[j]);
-      if (NORM == ROLA_NORM_HEAD || (NORM == ROLA_NORM_TOKEN && !ROT)) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[j][i] *= f;
+      for (int i = 0; i < P; ++i) {
+        if (NORM != ROLA_NORM_NONE) x[j][i] = __fmul2_rn(x[j][i], gain[j][i]);
+        if (NORM == ROLA_NORM_HEAD || (NORM == ROLA_NORM_TOKEN && !ROT)) x[j][i] = __fmul2_rn(x[j][i], make_float2(f, f));
       }
-      if (ROT) turn_piece<false, E>(cs, x[j]);
-      store_piece<E>(dst + n * so.n + j * ho, x[j]);
+      if (ROT) rotate<false>(cs, x[j]);
+      store_pairs<E>(dst + n * so.n + j * ho, x[j]);
     }
     slot = slot == kAhead - 1 ? 0 : slot + 1;
     turn = next;
@@ -292,6 +297,7 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward
     const __grid_constant__ NormRopeArgs a, int W, const TG* dqo, const TG* dko, const T* __restrict__ q,
     const T* __restrict__ k, const float* __restrict__ wq, const float* __restrict__ wk, T* dq, T* dk,
     float* __restrict__ part) {
+  constexpr int P = E / 2;
   constexpr int kBg = piece_bytes<E, TG>(), kBx = NORM == ROLA_NORM_NONE ? 0 : piece_bytes<E, T>();
   constexpr int kRow = V * (kBg + kBx);            // bytes of a row per thread
   __shared__ Shared sh;
@@ -306,17 +312,13 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward
   const TG* up = (is_k ? dko : dqo) + b * su.b + h0 * su.h + c;
   const int64_t hx = hs * si.h, hu = hs * su.h;
   T* dst = (is_k ? dk : dq) + ((size_t)b * a.N * a.H + h0) * a.d + c;
-  float gain[V][E], acc[V][E];
+  float2 gain[V][P], acc[V][P];
 #pragma unroll
-  for (int j = 0; j < V; ++j)
+  for (int j = 0; j < V; ++j) {
+    load_gain<NORM>(a, w, h0 + j * hs, c, gain[j]);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const bool on = h0 + j * hs < a.H;
-      gain[j][i] = NORM == ROLA_NORM_NONE || !on ? 0.f
-                   : NORM == ROLA_NORM_HEAD      ? __ldg(w + c + i)
-                                                 : __ldg(w + (size_t)(h0 + j * hs) * a.d + c + i);
-      acc[j][i] = 0.f;
-    }
+    for (int i = 0; i < P; ++i) acc[j][i] = make_float2(0.f, 0.f);
+  }
   const Turner turner(a, ROT == kPerToken ? rg.t : a.d, 32 * W);
   float2* tab = reinterpret_cast<float2*>(ring + kAhead * kRow * nt);
   const float inv = 1.f / (NORM == ROLA_NORM_TOKEN ? C : a.d);
@@ -346,30 +348,28 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward
   for (long long n = first; n < a.N; n += step, ++it) {
     fetch(n + (long long)(kAhead - 1) * step, slot == 0 ? kAhead - 1 : slot - 1);
     copy_wait<kAhead - 1>();
-    float2 cs[E / 2];
+    float2 cs[P];
     if (ROT == kTable) {
       walk.load(a, tab, cs);
       walk.next(a);
     } else if (ROT) {
       load_turns<E>(sh.cs[turn][rg.g] + (c >> 1), cs);
     }
-    float g[V][E];
+    float2 g[V][P];
     float s0 = 0.f, s1 = 0.f, r[V], m[V];   // sums of x^2 and of h x;  r = 1/rms, m = mean(h x r)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const bool on = h0 + j * hs < a.H;
       const uint8_t* at = ring + (slot * kRow + j * (kBg + kBx)) * nt;
-      read_piece<E, TG>(at, g[j]);
-      if (ROT) turn_piece<true, E>(cs, g[j]);
+      read_pairs<TG, E>(at, g[j]);
+      if (ROT) rotate<true>(cs, g[j]);
       if (NORM != ROLA_NORM_NONE) {
-        float x[E];                    // read again below: cheaper than V x E more registers
-        read_piece<E, T>(at + kBg * nt, x);
-        const float t0 = on ? dot_piece<E>(x, x) : 0.f;
-        float h[E];
+        float2 x[P], h[P];             // x is read again below: cheaper than V x E more registers
+        read_pairs<T, E>(at + kBg * nt, x);
+        const float t0 = on ? dot(x, x) : 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) h[i] = g[j][i];
-        mul_piece<E>(h, gain[j]);
-        const float t1 = on ? dot_piece<E>(h, x) : 0.f;
+        for (int i = 0; i < P; ++i) h[i] = __fmul2_rn(g[j][i], gain[j][i]);
+        const float t1 = on ? dot(h, x) : 0.f;
         s0 += t0;
         s1 += t1;
         if (NORM == ROLA_NORM_HEAD) {
@@ -394,19 +394,17 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward
     for (int j = 0; j < V; ++j) {
       if (h0 + j * hs >= a.H) continue;
       if (NORM != ROLA_NORM_NONE) {
-        float x[E];
-        read_piece<E, T>(ring + (slot * kRow + j * (kBg + kBx) + kBg) * nt, x);
+        float2 x[P];
+        read_pairs<T, E>(ring + (slot * kRow + j * (kBg + kBx) + kBg) * nt, x);
+        const float2 rr = make_float2(r[j], r[j]), mm = make_float2(-m[j], -m[j]);
 #pragma unroll
-        for (int i = 0; i < E; i += 2) sm100::mul2(x[i], x[i + 1], r[j], r[j]);   // x / rms
-        fma_piece<E>(acc[j], g[j], x);
-        mul_piece<E>(g[j], gain[j]);
-#pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          sm100::fma2(g[j][i], g[j][i + 1], x[i], x[i + 1], -m[j], -m[j], g[j][i], g[j][i + 1]);
-          sm100::mul2(g[j][i], g[j][i + 1], r[j], r[j]);
+        for (int i = 0; i < P; ++i) {
+          const float2 xh = __fmul2_rn(x[i], rr);               // x / rms
+          acc[j][i] = __ffma2_rn(g[j][i], xh, acc[j][i]);
+          g[j][i] = __fmul2_rn(__ffma2_rn(xh, mm, __fmul2_rn(g[j][i], gain[j][i])), rr);
         }
       }
-      store_piece<E>(dst + ((size_t)n * a.H + j * hs) * a.d, g[j]);
+      store_pairs<E>(dst + ((size_t)n * a.H + j * hs) * a.d, g[j]);
     }
     slot = slot == kAhead - 1 ? 0 : slot + 1;
     turn = next;
@@ -417,7 +415,7 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward
     float* p = part + (group * 2 + is_k) * C + (size_t)h0 * a.d + c;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (h0 + j * hs < a.H) store_floats<E>(p + (size_t)j * hs * a.d, acc[j]);
+      if (h0 + j * hs < a.H) store_floats<E>(p + (size_t)j * hs * a.d, &acc[j][0].x);
   }
 }
 

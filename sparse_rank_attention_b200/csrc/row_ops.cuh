@@ -30,7 +30,7 @@ inline RowShape row_shape(int C, int E, int max_v, int max_warps = kMaxRowWarps)
     const int w = (pieces + 32 * v - 1) / (32 * v);
     if (s.W > max_warps || 8ll * v * w <= 9ll * s.V * s.W) s.V = v, s.W = w;
   }
-  s.G = s.W >= 4 ? 1 : 4 / s.W;
+  s.G = s.W == 1 ? 4 : 1;   // groups of several warps have the block's barrier to themselves
   s.threads = 32 * s.W * s.G;
   return s;
 }
@@ -147,11 +147,10 @@ struct RowGroup {
     t = 32 * wi + lane;
   }
   __device__ __forceinline__ void sync() const {
-    if (W == 1) {
+    if (W == 1)
       __syncwarp();
-    } else {
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(32 * W) : "memory");
-    }
+    else
+      __syncthreads();   // the group is the block
   }
 };
 
