@@ -28,8 +28,9 @@ constexpr int kMaxV = 4;                       // pieces of a thread
 constexpr int kMaxThreads = 512;                // 8192 channels, pieces of 4
 constexpr int kMaxWarps = kMaxThreads / 32;
 
+template <bool kAngles>
 struct Shared {
-  alignas(16) float2 cs[3][kMaxGroups][64];   // written one token ahead: three in turn
+  alignas(16) float2 cs[kAngles ? 3 : 1][kMaxGroups][kAngles ? 64 : 1];   // written one token ahead: three in turn
   alignas(16) float red[2][kMaxGroups][2 * kMaxWarps];
 };
 
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
                                                         const float* __restrict__ wk, T* qo, T* ko) {
   constexpr int P = E / 2;
   constexpr int kRow = V * piece_bytes<E, T>();   // bytes of a row per thread
-  __shared__ Shared sh;
+  __shared__ Shared<ROT == kPerToken> sh;
   extern __shared__ __align__(16) uint8_t ring[];   // [kAhead][V][tensors][threads] pieces
   const RowGroup rg(W);
   const int G = blockDim.x / (32 * W), b = blockIdx.y, nt = blockDim.x;
@@ -293,14 +294,14 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
 
 // Backward.  dq, dk are contiguous.  part: [gridDim.x * B * G][2][H * d] partial sums of dw.
 template <typename T, typename TG, int E, int NORM, int ROT, int V>
-__global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_backward_kernel(
+__global__ void __launch_bounds__(kMaxThreads) norm_rope_backward_kernel(
     const __grid_constant__ NormRopeArgs a, int W, const TG* dqo, const TG* dko, const T* __restrict__ q,
     const T* __restrict__ k, const float* __restrict__ wq, const float* __restrict__ wk, T* dq, T* dk,
     float* __restrict__ part) {
   constexpr int P = E / 2;
   constexpr int kBg = piece_bytes<E, TG>(), kBx = NORM == ROLA_NORM_NONE ? 0 : piece_bytes<E, T>();
   constexpr int kRow = V * (kBg + kBx);            // bytes of a row per thread
-  __shared__ Shared sh;
+  __shared__ Shared<ROT == kPerToken> sh;
   extern __shared__ __align__(16) uint8_t ring[];   // [kAhead][V][tensors][threads] pieces
   const RowGroup rg(W);
   const int G = blockDim.x / (32 * W), b = blockIdx.y, nt = blockDim.x, C = a.H * a.d;
@@ -433,6 +434,9 @@ int token_blocks(const RowShape& s, int B, int N, int tensors) {
   return (int)(x < most ? x : most);
 }
 
+// Backward: a thread's sums of dw stay in registers, so half as many channels per thread.
+RowShape backward_shape(int C, int E) { return row_shape(C, E, 16 / E, kMaxWarps); }
+
 template <typename K>
 cudaError_t opt_in(K kern, size_t smem) {
   return smem <= 40 * 1024 ? cudaSuccess   // with the static part within the default
@@ -501,12 +505,14 @@ template <typename T, typename TG, int NORM>
 cudaError_t backward(const NormRopeArgs& a, const void* dqo, const void* dko, const void* q, const void* k,
                      const float* wq, const float* wk, void* dq, void* dk, float* dwq, float* dwk, float* part,
                      cudaStream_t st) {
-  const RowShape s = row_shape(a.H * a.d, kE<T, TG>, kMaxV, kMaxWarps);
+  const RowShape s = backward_shape(a.H * a.d, kE<T, TG>);
   auto go = [&](auto rot) {
     constexpr int R = decltype(rot)::value;
-    return s.V == 1   ? backward_v<T, TG, NORM, R, 1>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st)
-           : s.V == 2 ? backward_v<T, TG, NORM, R, 2>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st)
-                      : backward_v<T, TG, NORM, R, 4>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st);
+    if constexpr (kE<T, TG> == 4)
+      if (s.V == 4)
+        return backward_v<T, TG, NORM, R, 4>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st);
+    return s.V == 1 ? backward_v<T, TG, NORM, R, 1>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st)
+                    : backward_v<T, TG, NORM, R, 2>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st);
   };
   if (a.rot.pos == ROLA_POS_NONE) return go(std::integral_constant<int, kNoRot>{});
   return use_table(a, s, dko ? 2 : 1) ? go(std::integral_constant<int, kTable>{}) : go(std::integral_constant<int, kPerToken>{});
@@ -530,7 +536,7 @@ cudaError_t forward_norm(rola_qk_norm norm, const A&... x) {
 int norm_rope_parts(int B, int N, int C, int tensors) {
   int most = 0;
   for (int e : {4, 8}) {               // for either type of piece
-    const RowShape s = row_shape(C, e, kMaxV, kMaxWarps);
+    const RowShape s = backward_shape(C, e);
     const int n = token_blocks(s, B, N, tensors) * B * s.G;
     most = n > most ? n : most;
   }
