@@ -46,6 +46,8 @@ class RolaCrossParams(ctypes.Structure):
 
 
 # ---------------------------------------------------------------------------- checks
+# Everything that shapes, strides, types and devices decide is checked once per combination and
+# kept with the parameter struct that it gives; what a call passes on is only its addresses.
 
 
 def _need(ok, where, what, code=_INVALID):
@@ -53,31 +55,56 @@ def _need(ok, where, what, code=_INVALID):
         raise RolaError(code, f"{where}: {what}")
 
 
-def _dtype(t, where, name):
-    code = _TYPES.get(t.dtype)
-    if code is None:
-        raise RolaError(_UNSUPPORTED, f"{where}: {name} is {t.dtype}, not fp32 or bf16")
+class _Meta:
+    """What a call's checks see of a tensor."""
+    __slots__ = ("shape", "strides", "dtype", "device")
+
+    def __init__(self, m):
+        self.shape, self.strides, self.dtype, self.device = tuple(m[0]), m[1], m[2], m[3]
+
+    @property
+    def contiguous(self):
+        want = 1
+        for n, s in zip(reversed(self.shape), reversed(self.strides)):
+            if n != 1 and s != want:
+                return False
+            want *= n
+        return True
+
+
+def _m(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _metas(*ms):
+    return [None if m is None else _Meta(m) for m in ms]
+
+
+def _type(m, where, name):
+    code = _TYPES.get(m.dtype)
+    _need(code is not None, where, f"{name} is {m.dtype}, not fp32 or bf16", _UNSUPPORTED)
     return code
 
 
-def _same_device(where, first, *tensors):
-    _need(first.is_cuda, where, "tensors are not on a CUDA device")
-    for t in tensors:
-        _need(t is None or t.device == first.device, where, "tensors are on different devices")
+def _one_device(where, *metas):
+    devices = {m.device for m in metas if m is not None}
+    _need(-1 not in devices, where, "tensors are not on a CUDA device")
+    _need(len(devices) == 1, where, "tensors are on different devices")
 
 
-def _param(where, name, t, shape):
-    _need(t.dtype == torch.float32 and t.shape == shape and t.is_contiguous(), where,
+def _param(where, name, m, shape):
+    _need(m is None or (m.dtype == torch.float32 and m.shape == shape and m.contiguous), where,
           f"{name} is not a contiguous fp32 {list(shape)}")
 
 
 def _on_device(call):
-    """Runs `call` with the first tensor's device as the current one."""
+    """Runs `call` with its first tensor's device as the current one."""
     @functools.wraps(call)
     def run(*args, **kw):
         first = args[0] if args else next((t for t in kw.values() if isinstance(t, torch.Tensor)), None)
-        if isinstance(first, torch.Tensor) and first.is_cuda and first.get_device() != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
+        device = first.get_device() if isinstance(first, torch.Tensor) else -1
+        if device >= 0 and device != torch.cuda.current_device():
+            with torch.cuda.device(device):
                 return call(*args, **kw)
         return call(*args, **kw)
     return run
@@ -87,8 +114,12 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _on(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _new(t, dtype=None):
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def _workspace(nbytes, device):
@@ -104,55 +135,44 @@ def _sized(fn, p):
 # ---------------------------------------------------------------------------- qk_norm_rope
 
 
-@functools.lru_cache(maxsize=256)
-def _rope_params(shape, strides, dtype, grad_dtype, norm, eps, pos, grid, start, batched, pairs, base):
-    p = RolaNormRopeParams()
-    p.B, p.N, p.H, p.d = shape
-    p.dtype, p.grad_dtype, p.norm, p.eps, p.pos = dtype, grad_dtype, norm, eps, pos
-    p.grid_t, p.grid_h, p.grid_w = grid
-    p.start_t, p.start_h, p.start_w = start
-    p.positions_batched = batched
-    p.rope_pairs_t, p.rope_pairs_h, p.rope_pairs_w = pairs
-    p.rope_base = base
-    for name, s in zip(("q", "k", "dq_out", "dk_out"), strides):
-        setattr(p, name, (_I64 * 3)(*s[:3]))
-    return p, _sized(load().rola_qk_norm_rope_workspace_size, p)
-
-
-def _rope_setup(where, q, k, wq, wk, up, norm, eps, grid, start, positions, pairs, rope_base, rope):
-    first = up[0] if q is None else q
-    _need(first.dim() == 4, where, "q is not [B, N, H, d]")
-    shape = tuple(first.shape)
-    dtype = _dtype(first, where, "q")
+@functools.lru_cache(maxsize=512)
+def _rope(where, q, k, wq, wk, positions, dq_out, dk_out, norm, eps, grid, start, pairs, rope_base, rope):
+    """(params, workspace bytes) of a call; q is None for a backward without a norm."""
+    q, k, wq, wk, positions, dq_out, dk_out = _metas(q, k, wq, wk, positions, dq_out, dk_out)
+    first = dq_out if q is None else q
+    _need(len(first.shape) == 4, where, "q is not [B, N, H, d]")
+    B, N, H, d = first.shape
+    dtype = _type(first, where, "q")
     _need(norm in NORMS, where, f"norm {norm!r} is not one of {sorted(NORMS)}")
-    n = {"none": 0, "token": shape[2] * shape[3], "head": shape[3]}[norm]
-    for name, t in (("q", q), ("k", k)):
+    for name, t in (("q", q), ("k", k), ("dq_out", dq_out), ("dk_out", dk_out)):
         if t is not None:
-            _need(t.shape == shape and t.dtype == first.dtype and t.stride(3) == 1, where,
+            like = dq_out if name.startswith("d") else q
+            _need(t.shape == first.shape and t.dtype == like.dtype and (t.strides[3] == 1 or d == 1), where,
                   f"{name} differs from q in shape or type, or its channels are not contiguous")
-    for name, t in (("dq_out", up[0]), ("dk_out", up[1])):
-        if t is not None:
-            _need(t.shape == shape and t.dtype == up[0].dtype and t.stride(3) == 1, where,
-                  f"{name} differs from q in shape, or its channels are not contiguous")
-    for name, t in (("wq", wq), ("wk", wk)):
-        if t is not None:
-            _param(where, name, t, (n,))
-    pos, batched, grid_given = POS_NONE, 0, grid
-    grid, start = (1, 1, shape[1]) if grid is None else tuple(grid), tuple(start)
+    n = {"none": 0, "token": H * d, "head": d}[norm]
+    _need(norm != "none" or (wq is None and wk is None), where, "gains come with a norm")
+    _param(where, "wq", wq, (n,))
+    _param(where, "wk", wk, (n,))
+    p = RolaNormRopeParams()
+    p.B, p.N, p.H, p.d = B, N, H, d
+    p.dtype = dtype
+    p.grad_dtype = dtype if dq_out is None else _type(dq_out, where, "dq_out")
+    p.norm, p.eps, p.rope_base = NORMS[norm], eps, rope_base
+    p.pos = POS_GRID if rope else POS_NONE
+    p.grid_t, p.grid_h, p.grid_w = (1, 1, N) if grid is None else grid
+    p.start_t, p.start_h, p.start_w = start
+    p.rope_pairs_t, p.rope_pairs_h, p.rope_pairs_w = pairs
     if positions is not None:
-        _need(rope and grid_given is None, where, "positions come without a grid, and not with rope=False")
-        batched = int(positions.dim() == 3)
-        _need(positions.dtype == torch.int32 and positions.is_contiguous()
-              and tuple(positions.shape) in ((shape[1], 3), (shape[0], shape[1], 3)), where,
+        _need(rope and grid is None, where, "positions come without a grid, and not with rope=False")
+        _need(positions.dtype == torch.int32 and positions.contiguous
+              and positions.shape in ((N, 3), (B, N, 3)), where,
               "positions are not a contiguous int32 [N, 3] or [B, N, 3]")
-        pos, grid, start = POS_GIVEN, (1, 1, 1), (0, 0, 0)
-    elif rope:
-        pos = POS_GRID
-    _same_device(where, first, q, k, wq, wk, positions, *up)
-    strides = tuple(t.stride() if t is not None else (0, 0, 0) for t in (q, k, *up))
-    grad_dtype = dtype if up[0] is None else _dtype(up[0], where, "dq_out")
-    return _rope_params(shape, strides, dtype, grad_dtype, NORMS[norm], eps, pos, grid, start, batched, tuple(pairs),
-                        float(rope_base))
+        p.pos, p.positions_batched = POS_GIVEN, len(positions.shape) - 2
+    _one_device(where, q, k, wq, wk, positions, dq_out, dk_out)
+    for name, t in (("q", q), ("k", k), ("dq_out", dq_out), ("dk_out", dk_out)):
+        if t is not None:
+            setattr(p, name, (_I64 * 3)(*t.strides[:3]))
+    return ctypes.byref(p), _sized(load().rola_qk_norm_rope_workspace_size, p), p
 
 
 @_on_device
@@ -166,23 +186,20 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, *, norm="token", eps=1e-6, grid=No
     ``rope=False`` the norm alone.  ``out``: the two results' tensors, contiguous, or q and k
     themselves.  Returns (q_out, k_out), or q_out alone without k."""
     where = "rola_qk_norm_rope"
-    p, _ = _rope_setup(where, q, k, wq, wk, (None, None), norm, eps, grid, start, positions, pairs, rope_base, rope)
+    mq = _m(q)
+    p = _rope(where, mq, _m(k), _m(wq), _m(wk), _m(positions), None, None, norm, eps,
+              None if grid is None else tuple(grid), tuple(start), tuple(pairs), rope_base, rope)
     if out is None:
-        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        ko = None if k is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qo, ko = _new(q), None if k is None else _new(k)
     else:
         qo, ko = (out, None) if isinstance(out, torch.Tensor) else out
         for t, src in ((qo, q), (ko, k)):
-            if t is None and src is None:
-                continue
-            _need(t is not None and src is not None and t.shape == q.shape and t.dtype == q.dtype
-                  and t.device == q.device and (t.is_contiguous() or (t.data_ptr() == src.data_ptr()
-                                                                      and t.stride() == src.stride())), where,
-                  "out is neither contiguous like q nor the input itself")
-            _need(t.data_ptr() != src.data_ptr() or t.stride() == src.stride() or t.is_contiguous() == src.is_contiguous(),
-                  where, "out starts where the input does but has other strides")
-    _check(load().rola_qk_norm_rope(ctypes.byref(p), q.data_ptr(), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions),
-                                    qo.data_ptr(), _ptr(ko), _stream(stream)), where)
+            _need((t is None) == (src is None) and (t is None or (
+                t.shape == q.shape and t.dtype == q.dtype and t.device == q.device
+                and (t.stride() == src.stride() if t.data_ptr() == src.data_ptr() else t.is_contiguous()))), where,
+                "out is neither contiguous like q nor the input itself")
+    _check(load().rola_qk_norm_rope(p[0], q.data_ptr(), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), qo.data_ptr(),
+                                    _ptr(ko), _on(stream, mq[3])), where)
     return qo if k is None else (qo, ko)
 
 
@@ -194,72 +211,61 @@ def qk_norm_rope_backward(dq_out, dk_out=None, q=None, k=None, wq=None, wk=None,
     type or fp32 (as ``Plan.backward`` returns them).  Returns a dict: dq, dk of q's type, dwq,
     dwk fp32; entries that do not apply are None.  q and k may be left out for norm="none"."""
     where = "rola_qk_norm_rope_backward"
-    if norm == "none":
-        dtype = dq_out.dtype if q is None else q.dtype
-        wq = wk = None
-    else:
-        _need(q is not None and wq is not None and (dk_out is None) == (k is None), where,
-              "q, k and their gains are needed with a norm")
-        dtype = q.dtype
-    if norm == "none" and q is not None:      # only its type counts
-        p, need = _rope_setup(where, q, k, None, None, (dq_out, dk_out), norm, eps, grid, start, positions, pairs,
-                              rope_base, rope)
+    dtype = dq_out.dtype if q is None else q.dtype
+    if norm != "none":
+        _need(q is not None and wq is not None and (dk_out is None) == (k is None) == (wk is None), where,
+              "q, k and their gains come with a norm")
+    mu = _m(dq_out)
+    p = _rope(where, _m(q), _m(k), _m(wq), _m(wk), _m(positions), mu, _m(dk_out), norm, eps,
+              None if grid is None else tuple(grid), tuple(start), tuple(pairs), rope_base, rope)
+    if norm == "none":                        # only their type counts
         q = k = None
-    else:
-        p, need = _rope_setup(where, q, k, wq, wk, (dq_out, dk_out), norm, eps, grid, start, positions, pairs,
-                              rope_base, rope)
-    dev = dq_out.device
-    dq = torch.empty(dq_out.shape, dtype=dtype, device=dev)
-    dk = None if dk_out is None else torch.empty(dq_out.shape, dtype=dtype, device=dev)
-    dwq = None if wq is None else torch.empty_like(wq)
-    dwk = None if wk is None else torch.empty_like(wk)
-    ws = _workspace(need, dev)
+    dq, dk = _new(dq_out, dtype), None if dk_out is None else _new(dk_out, dtype)
+    dwq, dwk = None if wq is None else _new(wq), None if wk is None else _new(wk)
+    need = p[1]
+    ws = _workspace(need, dq_out.device)
     _check(load().rola_qk_norm_rope_backward(
-        ctypes.byref(p), dq_out.data_ptr(), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions),
-        dq.data_ptr(), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), need, _stream(stream)), where)
+        p[0], dq_out.data_ptr(), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), dq.data_ptr(),
+        _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), need, _on(stream, mu[3])), where)
     return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
 
 
 # ---------------------------------------------------------------------------- gated_norm
 
 
-@functools.lru_cache(maxsize=256)
-def _gated_params(shape, T, x_dtype, y_dtype, norm, eps, strides):
-    p = RolaGatedNormParams()
-    p.B, p.N, p.C = shape
-    p.T, p.x_dtype, p.y_dtype, p.norm, p.eps = T, x_dtype, y_dtype, norm, eps
-    p.gate_b, p.gate_t, p.scale_b, p.scale_t, p.shift_b, p.shift_t = strides
-    return p, _sized(load().rola_gated_norm_workspace_size, p)
-
-
-def _gated_setup(where, x, y_dtype, mods, norm, eps, like_x, like_y, params):
-    _need(x.dim() == 3, where, "x is not [B, N, C]")
+@functools.lru_cache(maxsize=512)
+def _gated(where, x, y_dtype, like_x, like_y, gate, scale, shift, weight, bias, norm, eps):
+    """(params, workspace bytes); like_x, like_y: tensors of x's shape in x's type, in y_dtype."""
+    x, gate, scale, shift, weight, bias = _metas(x, gate, scale, shift, weight, bias)
+    like_x, like_y = _metas(*like_x), _metas(*like_y)
+    _need(len(x.shape) == 3, where, "x is not [B, N, C]")
     _need(norm in KINDS, where, f"norm {norm!r} is not one of {sorted(KINDS)}")
     B, N, C = x.shape
-    y_code = _TYPES.get(y_dtype)
-    _need(y_code is not None, where, f"y is {y_dtype}, not fp32 or bf16", _UNSUPPORTED)
-    for name, t, dt in [(n, t, x.dtype) for n, t in like_x] + [(n, t, y_dtype) for n, t in like_y]:
-        if t is not None:
-            _need(t.shape == x.shape and t.dtype == dt and t.is_contiguous(), where,
-                  f"{name} is not a contiguous {dt} {list(x.shape)}")
-    T, strides = None, []
-    for name, m in mods:
+    p = RolaGatedNormParams()
+    p.B, p.N, p.C = x.shape
+    p.x_dtype = _type(x, where, "x")
+    _need(y_dtype in _TYPES, where, f"y is {y_dtype}, not fp32 or bf16", _UNSUPPORTED)
+    p.y_dtype, p.norm, p.eps = _TYPES[y_dtype], KINDS[norm], eps
+    for t, dt in [(x, x.dtype)] + [(t, x.dtype) for t in like_x] + [(t, y_dtype) for t in like_y]:
+        _need(t is None or (t.shape == x.shape and t.dtype == dt and t.contiguous), where,
+              f"a tensor beside x is not a contiguous {dt} {[B, N, C]}")
+    T = 0
+    for name, m in (("gate", gate), ("scale", scale), ("shift", shift)):
         if m is None:
-            strides += [0, 0]
             continue
-        _need(m.dtype == torch.float32 and m.stride(-1) == 1 and m.dim() in (2, 3), where,
+        _need(m.dtype == torch.float32 and len(m.shape) in (2, 3) and m.strides[-1] == 1, where,
               f"{name} is not an fp32 [B, C] or [B, T, C] with contiguous channels")
-        t = 1 if m.dim() == 2 else m.shape[1]
-        _need(m.shape[0] == B and m.shape[-1] == C and T in (None, t), where,
+        t = 1 if len(m.shape) == 2 else m.shape[1]
+        _need(m.shape[0] == B and m.shape[-1] == C and T in (0, t), where,
               f"{name} is not [B, T, C] with one T for all modulations")
         T = t
-        strides += [m.stride(0), m.stride(1) if m.dim() == 3 else 0]
-    for name, w in params:
-        if w is not None:
-            _param(where, name, w, (C,))
-    T = T or 1
-    _same_device(where, x, *(t for _, t in (*mods, *like_x, *like_y, *params)))
-    return _gated_params((B, N, C), T, _dtype(x, where, "x"), y_code, KINDS[norm], eps, tuple(strides))
+        setattr(p, name + "_b", m.strides[0])
+        setattr(p, name + "_t", m.strides[1] if len(m.shape) == 3 else 0)
+    p.T = T or 1
+    _param(where, "weight", weight, (C,))
+    _param(where, "bias", bias, (C,))
+    _one_device(where, x, *like_x, *like_y, gate, scale, shift, weight, bias)
+    return ctypes.byref(p), _sized(load().rola_gated_norm_workspace_size, p), p
 
 
 @_on_device
@@ -274,11 +280,10 @@ def gated_norm(x, branch=None, gate=None, scale=None, shift=None, weight=None, b
     where = "rola_gated_norm"
     if y_dtype is None:
         y_dtype = x.dtype if branch is None else branch.dtype
-    p, _ = _gated_setup(where, x, y_dtype, (("gate", gate), ("scale", scale), ("shift", shift)), norm, eps,
-                        (("x", x),), (("branch", branch),), (("weight", weight), ("bias", bias)))
+    mx = _m(x)
+    p = _gated(where, mx, y_dtype, (), (_m(branch),), _m(gate), _m(scale), _m(shift), _m(weight), _m(bias), norm, eps)
     if out is None:
-        r = None if branch is None else torch.empty_like(x)
-        y = torch.empty(x.shape, dtype=y_dtype, device=x.device)
+        r, y = None if branch is None else _new(x), _new(x, y_dtype)
     else:
         r, y = out
         r = None if branch is None else r
@@ -286,8 +291,8 @@ def gated_norm(x, branch=None, gate=None, scale=None, shift=None, weight=None, b
             _need((t is None and t is r and branch is None)
                   or (t is not None and t.shape == x.shape and t.dtype == dt and t.is_contiguous()
                       and t.device == x.device), where, "out is not a pair of contiguous tensors like x and y")
-    _check(load().rola_gated_norm(ctypes.byref(p), x.data_ptr(), _ptr(branch), _ptr(gate), _ptr(scale), _ptr(shift),
-                                  _ptr(weight), _ptr(bias), _ptr(r), y.data_ptr(), _stream(stream)), where)
+    _check(load().rola_gated_norm(p[0], x.data_ptr(), _ptr(branch), _ptr(gate), _ptr(scale), _ptr(shift),
+                                  _ptr(weight), _ptr(bias), _ptr(r), y.data_ptr(), _on(stream, mx[3])), where)
     return (x if r is None else r), y
 
 
@@ -299,54 +304,49 @@ def gated_norm_backward(dy, r, dr=None, branch=None, gate=None, scale=None, weig
     dict: dx, dbranch, dgate, dscale, dshift (in the modulations' shape), dweight, dbias;
     entries that do not apply are None."""
     where = "rola_gated_norm_backward"
-    p, need = _gated_setup(where, r, dy.dtype, (("gate", gate), ("scale", scale), ("shift", None)), norm, eps,
-                           (("r", r), ("dr", dr)), (("dy", dy), ("branch", branch)), (("weight", weight),))
-    dev = r.device
-
-    def like(t, dtype=None):
-        return None if t is None else torch.empty(t.shape, dtype=dtype or t.dtype, device=dev)
-
-    res = {"dx": like(r), "dbranch": like(branch), "dgate": like(gate), "dscale": like(scale), "dshift": like(scale),
-           "dweight": like(weight), "dbias": like(weight)}
-    ws = _workspace(need, dev)
+    mr = _m(r)
+    p = _gated(where, mr, dy.dtype, (_m(dr),), (_m(dy), _m(branch)), _m(gate), _m(scale), None, _m(weight), None, norm,
+               eps)
+    res = {"dx": _new(r), "dbranch": None if branch is None else _new(branch)}
+    for name, t in (("dgate", gate), ("dscale", scale), ("dshift", scale), ("dweight", weight), ("dbias", weight)):
+        res[name] = None if t is None else _new(t)
+    need = p[1]
+    ws = _workspace(need, r.device)
     _check(load().rola_gated_norm_backward(
-        ctypes.byref(p), dy.data_ptr(), _ptr(dr), r.data_ptr(), _ptr(branch), _ptr(gate), _ptr(scale), _ptr(weight),
-        *[_ptr(t) for t in res.values()], _ptr(ws), need, _stream(stream)), where)
+        p[0], dy.data_ptr(), _ptr(dr), r.data_ptr(), _ptr(branch), _ptr(gate), _ptr(scale), _ptr(weight),
+        *[_ptr(t) for t in res.values()], _ptr(ws), need, _on(stream, mr[3])), where)
     return res
 
 
 # ---------------------------------------------------------------------------- cross_attend
 
 
-@functools.lru_cache(maxsize=256)
-def _cross_params(q_shape, Nk, dtype, scale, strides):
-    p = RolaCrossParams()
-    p.B, p.Nq, p.H, p.d = q_shape
-    p.Nk, p.dtype, p.softmax_scale = Nk, dtype, scale
-    for name, s in zip(("q", "k", "v", "dout"), strides):
-        setattr(p, name, (_I64 * 3)(*s[:3]))
-    lib = load()
-    return p, _sized(lib.rola_cross_workspace_size, p), _sized(lib.rola_cross_backward_workspace_size, p)
-
-
-def _cross_setup(where, q, k, v, kv_len, key_mask, softmax_scale, dout=None):
-    _need(q.dim() == 4 and k.dim() == 4, where, "q is not [B, Nq, H, d], or k not [B, Nk, H, d]")
-    B, _, H, d = q.shape
+@functools.lru_cache(maxsize=512)
+def _cross(where, q, k, v, kv_len, key_mask, dout, out, lse, softmax_scale):
+    """(params, workspace bytes of the forward, of the backward)."""
+    q, k, v, kv_len, key_mask, dout, out, lse = _metas(q, k, v, kv_len, key_mask, dout, out, lse)
+    _need(len(q.shape) == 4 and len(k.shape) == 4, where, "q is not [B, Nq, H, d], or k not [B, Nk, H, d]")
+    B, Nq, H, d = q.shape
     Nk = k.shape[1]
-    for name, t, shape in (("q", q, q.shape), ("k", k, (B, Nk, H, d)), ("v", v, (B, Nk, H, d)),
-                           ("dout", dout, q.shape)):
+    p = RolaCrossParams()
+    p.B, p.Nq, p.Nk, p.H, p.d = B, Nq, Nk, H, d
+    p.dtype, p.softmax_scale = _type(q, where, "q"), softmax_scale
+    for name, t, n in (("q", q, Nq), ("k", k, Nk), ("v", v, Nk), ("dout", dout, Nq)):
         if t is not None:
-            _need(t.shape == shape and t.dtype == q.dtype and t.stride(3) == 1, where,
-                  f"{name} is not a {q.dtype} {list(shape)} with contiguous channels")
-    if kv_len is not None:
-        _need(kv_len.dtype == torch.int32 and kv_len.shape == (B,) and kv_len.is_contiguous(), where,
-              "kv_len is not a contiguous int32 [B]")
-    if key_mask is not None:
-        _need(key_mask.dtype in (torch.bool, torch.uint8) and key_mask.shape == (B, Nk) and key_mask.is_contiguous(),
-              where, "key_mask is not a contiguous bool or uint8 [B, Nk]")
-    _same_device(where, q, k, v, kv_len, key_mask, dout)
-    strides = (q.stride(), k.stride(), v.stride(), (0, 0, 0) if dout is None else dout.stride())
-    return _cross_params(tuple(q.shape), Nk, _dtype(q, where, "q"), float(softmax_scale), strides)
+            _need(t.shape == (B, n, H, d) and t.dtype == q.dtype and (t.strides[3] == 1 or d == 1), where,
+                  f"{name} is not a {q.dtype} {[B, n, H, d]} with contiguous channels")
+            setattr(p, name, (_I64 * 3)(*t.strides[:3]))
+    _need(kv_len is None or (kv_len.dtype == torch.int32 and kv_len.shape == (B,) and kv_len.contiguous), where,
+          "kv_len is not a contiguous int32 [B]")
+    _need(key_mask is None or (key_mask.dtype in (torch.bool, torch.uint8) and key_mask.shape == (B, Nk)
+                               and key_mask.contiguous), where, "key_mask is not a contiguous bool or uint8 [B, Nk]")
+    _need(out is None or (out.shape == q.shape and out.dtype == q.dtype and out.contiguous), where,
+          "out is not contiguous like q")
+    _need(lse is None or (lse.shape == (B, H, Nq) and lse.dtype == torch.float32 and lse.contiguous), where,
+          "lse is not the forward's")
+    _one_device(where, q, k, v, kv_len, key_mask, dout, out, lse)
+    lib = load()
+    return ctypes.byref(p), _sized(lib.rola_cross_workspace_size, p), _sized(lib.rola_cross_backward_workspace_size, p), p
 
 
 @_on_device
@@ -356,16 +356,16 @@ def cross_attend(q, k, v, *, kv_len=None, key_mask=None, softmax_scale=0.0, retu
     uint8 [B, Nk]); a sample without keys gives zeros.  softmax_scale 0: 1/sqrt(d).  Returns
     out [B, Nq, H, d], with ``return_lse`` also the log sum of exponentials fp32 [B, H, Nq]."""
     where = "rola_cross_attend"
-    p, need, _ = _cross_setup(where, q, k, v, kv_len, key_mask, softmax_scale)
+    mq = _m(q)
+    p = _cross(where, mq, _m(k), _m(v), _m(kv_len), _m(key_mask), None, _m(out), None, softmax_scale)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == q.device, where,
-              "out is not contiguous like q")
-    lse = torch.empty((p.B, p.H, p.Nq), dtype=torch.float32, device=q.device) if return_lse else None
+        out = _new(q)
+    B, Nq, H, _ = mq[0]
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if return_lse else None
+    need = p[1]
     ws = _workspace(need, q.device)
-    _check(load().rola_cross_attend(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_len),
-                                    _ptr(key_mask), out.data_ptr(), _ptr(lse), _ptr(ws), need, _stream(stream)), where)
+    _check(load().rola_cross_attend(p[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_len), _ptr(key_mask),
+                                    out.data_ptr(), _ptr(lse), _ptr(ws), need, _on(stream, mq[3])), where)
     return (out, lse) if return_lse else out
 
 
@@ -374,20 +374,18 @@ def cross_attend_backward(dout, q, k, v, out, lse, *, kv_len=None, key_mask=None
     """Gradients of ``cross_attend`` from dout, with the forward's inputs, out and lse.  Returns
     a dict: dq, dk, dv, contiguous and of q's type."""
     where = "rola_cross_attend_backward"
-    p, _, need = _cross_setup(where, q, k, v, kv_len, key_mask, softmax_scale, dout)
-    _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and lse.dtype == torch.float32
-          and tuple(lse.shape) == (p.B, p.H, p.Nq) and lse.is_contiguous(), where,
-          "out and lse are not the forward's results")
-    _same_device(where, q, out, lse)
-    res = {n: torch.empty(t.shape, dtype=q.dtype, device=q.device) for n, t in (("dq", q), ("dk", k), ("dv", v))}
+    mq = _m(q)
+    p = _cross(where, mq, _m(k), _m(v), _m(kv_len), _m(key_mask), _m(dout), _m(out), _m(lse), softmax_scale)
+    dq, dk, dv = _new(q), _new(k), _new(v)
+    need = p[2]
     ws = _workspace(need, q.device)
     _check(load().rola_cross_attend_backward(
-        ctypes.byref(p), dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-        _ptr(kv_len), _ptr(key_mask), *[t.data_ptr() for t in res.values()], _ptr(ws), need, _stream(stream)), where)
-    return res
+        p[0], dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), _ptr(kv_len),
+        _ptr(key_mask), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws), need, _on(stream, mq[3])), where)
+    return {"dq": dq, "dk": dk, "dv": dv}
 
 
 def block_poll_status(stream=None) -> int:
     """Synchronises the stream; returns the status code of the calls of this module on the
     current device since the last poll (0 = ok), clearing it."""
-    return load().rola_block_poll_status(_stream(stream))
+    return load().rola_block_poll_status((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
