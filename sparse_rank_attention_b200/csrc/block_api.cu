@@ -481,7 +481,8 @@ rola_status rola_cross_attend(const rola_cross_params* p, const void* q, const v
   float* part = static_cast<float*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (p->dtype == ROLA_F32)
-    return cuda_status(rola::launch_cross_simt(a, p->dtype, splits, q, k, v, out, lse, part, st));
+    return cuda_status(rola::launch_cross_simt(a, splits, static_cast<const float*>(q), static_cast<const float*>(k),
+                                               static_cast<const float*>(v), static_cast<float*>(out), lse, part, st));
   return cuda_status(rola::launch_cross_sm100(a, splits, q, k, v, out, lse, part, st));
 }
 
@@ -528,8 +529,10 @@ rola_status rola_cross_attend_backward(const rola_cross_params* p, const void* d
   const CrossArgs a = args_of(*p, kv_len, key_mask);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (p->dtype == ROLA_F32)
-    return cuda_status(rola::launch_cross_simt_backward(a, p->dtype, sp.queries, sp.keys, dout, q, k, v, out, lse, dq,
-                                                        dk, dv, stats, part, st));
+    return cuda_status(rola::launch_cross_simt_backward(
+        a, sp.queries, sp.keys, static_cast<const float*>(dout), static_cast<const float*>(q),
+        static_cast<const float*>(k), static_cast<const float*>(v), static_cast<const float*>(out), lse,
+        static_cast<float*>(dq), static_cast<float*>(dk), static_cast<float*>(dv), stats, part, st));
   return cuda_status(rola::launch_cross_sm100_backward(a, sp.queries, sp.keys, dout, q, k, v, out, lse, dq, dk, dv,
                                                        stats, part, st));
 }

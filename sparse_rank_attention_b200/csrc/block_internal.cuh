@@ -82,10 +82,11 @@ cudaError_t launch_cross_join(const CrossArgs& a, rola_dtype dt, int splits, con
 cudaError_t launch_cross_sum(rola_dtype dt, int parts, size_t n, size_t stride, const float* part, void* out,
                              cudaStream_t st);
 // splits_k: blocks that share a query tile's keys; splits_q: blocks that share a key tile's queries.
-cudaError_t launch_cross_simt(const CrossArgs& a, rola_dtype dt, int splits_k, const void* q, const void* k,
-                              const void* v, void* out, float* lse, float* part, cudaStream_t st);
-cudaError_t launch_cross_simt_backward(const CrossArgs& a, rola_dtype dt, int splits_q, int splits_k, const void* dout,
-                                       const void* q, const void* k, const void* v, const void* out, const float* lse,
-                                       void* dq, void* dk, void* dv, float* drow, float* part, cudaStream_t st);
+cudaError_t launch_cross_simt(const CrossArgs& a, int splits_k, const float* q, const float* k, const float* v,
+                              float* out, float* lse, float* part, cudaStream_t st);
+cudaError_t launch_cross_simt_backward(const CrossArgs& a, int splits_q, int splits_k, const float* dout,
+                                       const float* q, const float* k, const float* v, const float* out,
+                                       const float* lse, float* dq, float* dk, float* dv, float* drow, float* part,
+                                       cudaStream_t st);
 
 }  // namespace rola
