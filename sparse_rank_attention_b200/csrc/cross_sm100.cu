@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
         fail |= !mbar_wait(bar(ctl->s_full[s]), step & 1, wc);
         if (__any_sync(0xffffffffu, fail)) break;
         tc_fence_after();
+        // The scores stay in registers from the maximum to the exponentials.
         float v[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, v + 32 * c);
@@ -275,40 +276,39 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
         const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sl2;   // sl2 > 0
         // rows whose offset moves: from nothing (O and l hold nothing yet), or by more than kSlack
         const bool move = mx > m + kSlack;                    // m = -inf: true for any finite score
-        float keep = 1.f;
-        if (move) {
-          keep = ex2_approx(m - mx);                          // 2^-inf = 0
-          m = mx;
+        if (__any_sync(0xffffffffu, move)) {
+          const float keep = move ? ex2_approx(m - mx) : 1.f;   // 2^-inf = 0
+          if (move) m = mx;
           l *= keep;
-        }
-        if (t > x.t0 && __any_sync(0xffffffffu, move)) {
-          float o[32];
+          if (t > x.t0) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            tmem_ld32(t_o + c, o);
-            tmem_wait_ld();
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tmem_ld16(t_o + c, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= keep;
-            tmem_st32(t_o + c, o);
+              for (int e = 0; e < 16; ++e) o[e] *= keep;
+              tmem_st16(t_o + c, o);
+            }
           }
         }
         const float off = m == -INFINITY ? 0.f : -m;          // no score yet: P = 2^-inf = 0
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 s2 = make_float2(sl2, sl2), o2 = make_float2(off, off);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           float pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float p0, p1;
-            fma2(p0, p1, v[c + e], v[c + e + 1], sl2, sl2, off, off);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            add2(sum[e & 2], sum[(e & 2) + 1], p0, p1);
-            pk[e >> 1] = __uint_as_float(pack_bf16(p0, p1));
+            float2 p = __ffma2_rn(make_float2(v[c + e], v[c + e + 1]), s2, o2);
+            p.x = ex2_approx(p.x);
+            p.y = ex2_approx(p.y);
+            sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], p);
+            pk[e >> 1] = __uint_as_float(pack_bf16(p.x, p.y));
           }
           tmem_st16(t_s + (c >> 1), pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
