@@ -94,7 +94,7 @@ struct DqGeo {
   static constexpr uint32_t kColO = 256;               // dQ of A, B
 };
 struct DqCtl {
-  uint64_t q_full[2], q_empty[2], do_full[2], do_empty[2], kv_full[6], k_ready[6], kv_empty[6];
+  uint64_t q_full[2], q_empty[2], do_full[2], do_empty[2], k_full[6], v_full[6], k_ready[6], kv_empty[6];
   uint64_t s_full[2], p_read[2], dp_full[2], ds_full[2], dq_done[2], o_free[2], drain;
   uint32_t tmem;
   int abort;
@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_sm100_kernel(
       mbar_init(bar(ctl->o_free[s]), 8);
     }
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(ctl->kv_full[s]), 1);
+      mbar_init(bar(ctl->k_full[s]), 1);
+      mbar_init(bar(ctl->v_full[s]), 1);
       mbar_init(bar(ctl->k_ready[s]), 1);
       mbar_init(bar(ctl->kv_empty[s]), 1);
     }
@@ -153,25 +154,27 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_sm100_kernel(
   if (warp == 0) {
     // ------------------------------------------------------------ loads: Q, dO; K, V, K, V, ...
     if (lane == 0) {
-      int nq[2] = {0, 0}, nkv = 0;
+      int nq[2] = {0, 0}, nkv = 0, nk = 0, nv = 0;   // items of A, B; K and V tiles; K; V
       bool ok = true;
       Item x{};
       auto load = [&](uint32_t dst, const CUtensorMap* tm, int n, uint32_t full) {
         mbar_expect_tx(full, G::kTileBytes);
         for (int c = 0; c < G::kBoxes; ++c) tma_load_4d(dst + c * kBox, tm, 64 * c, x.h, n, x.b, full);
       };
-      auto load_kv = [&](const CUtensorMap* tm, int t) {
+      // K and V tiles share the slots in turn; each kind has its own full barriers, as in the forward
+      auto load_kv = [&](const CUtensorMap* tm, uint64_t* full, int& n, int t) {
         const int s = R::slot(nkv);
         if (nkv >= kStages && !mbar_wait(bar(ctl->kv_empty[s]), R::empty(nkv), wc)) return false;
-        load(sbase + G::kOffKV + s * G::kTileBytes, tm, t * kTile, bar(ctl->kv_full[s]));
+        load(sbase + G::kOffKV + s * G::kTileBytes, tm, t * kTile, bar(full[R::slot(n)]));
         ++nkv;
+        ++n;
         return true;
       };
       for (int i = next_item(a, w, blockIdx.x, &x); ok && i < w.items; i = next_item(a, w, i + gridDim.x, &x)) {
         for (int s = 0; ok && s < x.streams; ++s) {
           if (nq[s] >= 1 && !mbar_wait(bar(ctl->q_empty[s]), (nq[s] - 1) & 1, wc)) { ok = false; break; }
           load(sbase + G::kOffQ + s * G::kTileBytes, &tm_q, x.q0 + s * kTile, bar(ctl->q_full[s]));
-          if (s == 0) ok = load_kv(&tm_k, x.t0);
+          if (s == 0) ok = load_kv(&tm_k, ctl->k_full, nk, x.t0);
         }
         for (int s = 0; ok && s < x.streams; ++s) {
           if (nq[s] >= 1 && !mbar_wait(bar(ctl->do_empty[s]), (nq[s] - 1) & 1, wc)) { ok = false; break; }
@@ -179,8 +182,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_sm100_kernel(
           ++nq[s];
         }
         for (int t = x.t0; ok && t < x.t1; ++t) {
-          ok = load_kv(&tm_v, t);
-          if (ok && t + 1 < x.t1) ok = load_kv(&tm_k, t + 1);
+          ok = load_kv(&tm_v, ctl->v_full, nv, t);
+          if (ok && t + 1 < x.t1) ok = load_kv(&tm_k, ctl->k_full, nk, t + 1);
         }
         if (!ok) {   // a Q whose dO was not issued: it too lands before the block leaves
           for (int s = 0; s < 2; ++s) mbar_wait(bar(ctl->q_full[s]), nq[s] & 1, wc, false);
@@ -191,8 +194,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_sm100_kernel(
           mbar_wait(bar(ctl->q_full[s]), (nq[s] - 1) & 1, wc, false);
           mbar_wait(bar(ctl->do_full[s]), (nq[s] - 1) & 1, wc, false);
         }
-      for (int y = nkv > kStages ? nkv - kStages : 0; y < nkv; ++y)
-        mbar_wait(bar(ctl->kv_full[R::slot(y)]), R::full(y), wc, false);
+      for (int y = nk > kStages ? nk - kStages : 0; y < nk; ++y)
+        mbar_wait(bar(ctl->k_full[R::slot(y)]), R::full(y), wc, false);
+      for (int y = nv > kStages ? nv - kStages : 0; y < nv; ++y)
+        mbar_wait(bar(ctl->v_full[R::slot(y)]), R::full(y), wc, false);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
@@ -234,7 +239,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_sm100_kernel(
           const int n_k = nkv, n_v = nkv + 1, n_next = nkv + 2;
           for (int s = 0; ok && s < x.streams; ++s) {           // dP = dO V^T once P has been read
             if (first && !mbar_wait(bar(ctl->do_full[s]), nq[s] & 1, wc)) { ok = false; break; }
-            if (!mbar_wait(bar(ctl->kv_full[R::slot(n_v)]), R::full(n_v), wc) ||
+            if (!mbar_wait(bar(ctl->v_full[R::slot(nkt)]), R::full(nkt), wc) ||   // V tile as many as K tile
                 !mbar_wait(bar(ctl->p_read[s]), steps[s] & 1, wc)) { ok = false; break; }
             score(s, sbase + G::kOffDo, n_v);
             mma_commit(bar(ctl->dp_full[s]));
@@ -284,7 +289,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_sm100_kernel(
         const int n = 2 * nkt, s = R::slot(n);
         uint32_t bits[4];
         tile_bits(a, x.b, len, t, lane, bits);
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(ctl->kv_full[s]), R::full(n), wc));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(ctl->k_full[R::slot(nkt)]), R::full(nkt), wc));
         if (!ok) break;
         if (!all_set(bits)) {
           clear_rows<G::kBoxes>(base + G::kOffKV + s * G::kTileBytes, bits, lane);

@@ -51,7 +51,7 @@ struct Geo {
 };
 
 struct Ctl {
-  uint64_t q_full[2], q_empty[2], kv_full[6], v_ready[6], kv_empty[6], s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t q_full[2], q_empty[2], k_full[6], v_full[6], v_ready[6], kv_empty[6], s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t drain;
   uint32_t tmem;
   int abort;
@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
       mbar_init(bar(ctl->o_free[s]), 4);
     }
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(ctl->kv_full[s]), 1);
+      mbar_init(bar(ctl->k_full[s]), 1);
+      mbar_init(bar(ctl->v_full[s]), 1);
       mbar_init(bar(ctl->v_ready[s]), 1);
       mbar_init(bar(ctl->kv_empty[s]), 1);
     }
@@ -109,18 +110,21 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      int nq[2] = {0, 0}, nkv = 0;
+      int nq[2] = {0, 0}, nkv = 0, nk = 0, nv = 0;   // tiles loaded: Q of A, B; K and V; K; V
       bool ok = true;
       Item x{};
       auto load = [&](uint32_t dst, const CUtensorMap* tm, int h, int n, int b, uint32_t full) {
         mbar_expect_tx(full, G::kTileBytes);
         for (int c = 0; c < G::kBoxes; ++c) tma_load_4d(dst + c * kBox, tm, 64 * c, h, n, b, full);
       };
-      auto load_kv = [&](const CUtensorMap* tm, int t) {
+      // K and V tiles share the ring's slots in turn, but each kind has its own full barriers: who
+      // waits for one kind alone then sees every phase of its barriers.
+      auto load_kv = [&](const CUtensorMap* tm, uint64_t* full, int& n, int t) {
         const int s = nkv % kStages;
         if (nkv >= kStages && !mbar_wait(bar(ctl->kv_empty[s]), ((nkv / kStages) - 1) & 1, wc)) return false;
-        load(sbase + G::kOffKV + s * G::kTileBytes, tm, x.h, t * kTile, x.b, bar(ctl->kv_full[s]));
+        load(sbase + G::kOffKV + s * G::kTileBytes, tm, x.h, t * kTile, x.b, bar(full[n % kStages]));
         ++nkv;
+        ++n;
         return true;
       };
       for (int i = next_item(a, w, blockIdx.x, &x); ok && i < w.items; i = next_item(a, w, i + gridDim.x, &x)) {
@@ -128,34 +132,36 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
           if (nq[s] >= 1 && !mbar_wait(bar(ctl->q_empty[s]), (nq[s] - 1) & 1, wc)) { ok = false; break; }
           load(sbase + G::kOffQ + s * G::kTileBytes, &tm_q, x.h, x.q0 + s * kTile, x.b, bar(ctl->q_full[s]));
           ++nq[s];
-          if (s == 0) ok = load_kv(&tm_k, x.t0);   // the first K right behind the first Q
+          if (s == 0) ok = load_kv(&tm_k, ctl->k_full, nk, x.t0);   // the first K right behind the first Q
         }
         for (int t = x.t0; ok && t < x.t1; ++t) {
-          ok = load_kv(&tm_v, t);
-          if (ok && t + 1 < x.t1) ok = load_kv(&tm_k, t + 1);
+          ok = load_kv(&tm_v, ctl->v_full, nv, t);
+          if (ok && t + 1 < x.t1) ok = load_kv(&tm_k, ctl->k_full, nk, t + 1);
         }
       }
       // every issued copy lands before the block leaves
       for (int s = 0; s < 2; ++s)
         if (nq[s] > 0) mbar_wait(bar(ctl->q_full[s]), (nq[s] - 1) & 1, wc, false);
-      for (int y = nkv > kStages ? nkv - kStages : 0; y < nkv; ++y)
-        mbar_wait(bar(ctl->kv_full[y % kStages]), (y / kStages) & 1, wc, false);
+      for (int y = nk > kStages ? nk - kStages : 0; y < nk; ++y)
+        mbar_wait(bar(ctl->k_full[y % kStages]), (y / kStages) & 1, wc, false);
+      for (int y = nv > kStages ? nv - kStages : 0; y < nv; ++y)
+        mbar_wait(bar(ctl->v_full[y % kStages]), (y / kStages) & 1, wc, false);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_f16(1, 128, 128, 0, 0), idesc_o = idesc_f16(1, 128, D, 0, 1);
       int steps[2] = {0, 0}, nq[2] = {0, 0}, no[2] = {0, 0};   // tiles, items of a stream
-      int nkv = 0, nvt = 0;                                     // K and V tiles, V tiles alone
+      int nkv = 0, nkt = 0, nvt = 0;                            // K and V tiles, of each kind alone
       bool ok = true;
       auto kv_wait = [&](uint64_t* full, int n) {
         return mbar_wait(bar(full[n % kStages]), (n / kStages) & 1, wc);
       };
-      // S_s = Q_s K^T; K is the nkv'th loaded tile.  P of the stream's previous tile lies where S
+      // S_s = Q_s K^T; K is the nkt'th K tile, in the slot of the n'th tile.  P of the stream's previous tile lies where S
       // goes, so its product with V must be done.
       auto issue_s = [&](int s, int n, bool first, bool last) {
         if (first && !mbar_wait(bar(ctl->q_full[s]), nq[s] & 1, wc)) return false;
-        if (!kv_wait(ctl->kv_full, n)) return false;
+        if (!kv_wait(ctl->k_full, nkt)) return false;
         if (steps[s] > 0 && !mbar_wait(bar(ctl->pv_done[s]), (steps[s] - 1) & 1, wc)) return false;
         tc_fence_after();
         const uint64_t dq = sdesc_sw128(sbase + G::kOffQ + s * G::kTileBytes, 16, 1024);
@@ -178,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
         for (int s = 0; ok && s < x.streams; ++s) ok = issue_s(s, nkv, true, x.t1 == x.t0 + 1);
         if (ok) mma_commit(bar(ctl->kv_empty[nkv % kStages]));
         ++nkv;
+        ++nkt;
       }
       while (ok && i < w.items) {
         const int i2 = next_item(a, w, i + gridDim.x, &y);
@@ -206,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
           }
           if (ok && any) mma_commit(bar(ctl->kv_empty[nk % kStages]));
           nkv += 1 + any;
+          nkt += any;
           ++nvt;
         }
         x = y;
@@ -225,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
         const int n = nkv + 2 * (t - x.t0) + 1, s = n % kStages;
         uint32_t bits[4];
         tile_bits(a, x.b, len, t, lane, bits);
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(ctl->kv_full[s]), (n / kStages) & 1, wc));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(ctl->v_full[nvt % kStages]), (nvt / kStages) & 1, wc));
         if (!ok) break;
         if (!all_set(bits)) {
           clear_rows<G::kBoxes>(base + G::kOffKV + s * G::kTileBytes, bits, lane);

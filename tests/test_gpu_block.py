@@ -299,3 +299,24 @@ def test_cross_attend_growing_scores():
             out, lse = rola.cross_attend(q, kk.contiguous(), v, return_lse=True)
             L.assert_within(out, want, oe, "out")
             L.assert_within(lse, wz, ze, "lse")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_cross_attend_repeats_bit_by_bit(d):
+    """Many key tiles through the rings of several blocks, again and again beside another
+    stream's traffic: every call gives the same bits and none of its waits runs out."""
+    g, q, k, v, _, _ = _cross_inputs(1, 2000, 3001, 8, d, BF16, None, None, 12)
+    dout = L.rand(g, 1, 2000, 8, d, dtype=BF16)
+    out, lse = rola.cross_attend(q, k, v, return_lse=True)
+    want = rola.cross_attend_backward(dout, q, k, v, out, lse)
+    other = torch.cuda.Stream()
+    big = torch.empty(64 << 20, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(40):
+        with torch.cuda.stream(other):
+            big.mul_(1.0)                                          # moves the loads' arrival around
+        again = rola.cross_attend(q, k, v, return_lse=True)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+        got = rola.cross_attend_backward(dout, q, k, v, out, lse)
+        assert all(torch.equal(got[n], want[n]) for n in got)
+    assert rola.block_poll_status() == 0
