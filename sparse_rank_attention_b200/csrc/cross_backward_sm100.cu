@@ -769,6 +769,7 @@ cudaError_t backward(const CrossArgs& a, int splits_q, int splits_k, const void*
   w.splits = splits_k;
   w.run = (ktiles + splits_k - 1) / splits_k;
   w.padded = padded;
+  set_divisors(&w, a.H);
   const long long items = (long long)a.B * a.H * w.pairs * splits_k;
   if (items > INT_MAX - 4096) return cudaErrorInvalidValue;
   w.items = (int)items;

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl* ctl = reinterpret_cast<Ctl*>(base + G::kOffCtl);
   const uint32_t sbase = smem_addr(base);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   auto bar = [&](uint64_t& m) { return smem_addr(&m); };
 
   if (threadIdx.x == 0) {
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
   const WaitCtl wc{&ctl->abort, g_status, limit_cycles};
 
   if (warp == 0) {
@@ -149,40 +149,38 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16(1, 128, 128, 0, 0), idesc_o = idesc_f16(1, 128, D, 0, 1);
+    {
       int steps[2] = {0, 0}, nq[2] = {0, 0}, no[2] = {0, 0};   // tiles, items of a stream
       int nkv = 0, nkt = 0, nvt = 0;                            // K and V tiles, of each kind alone
       bool ok = true;
-      auto kv_wait = [&](uint64_t* full, int n) {
-        return mbar_wait(bar(full[n % kStages]), (n / kStages) & 1, wc);
+      auto wait = [&](uint64_t& m, uint32_t parity) { return warp_wait(m, parity, wc); };
+      auto kv_wait = [&](uint64_t* full, int n) { return wait(full[n % kStages], (n / kStages) & 1); };
+      auto slot = [&](int n) { return sbase + G::kOffKV + (n % kStages) * G::kTileBytes; };
+      auto commit = [&](uint64_t& m) {
+        if (elect_leader()) mma_commit(bar(m));
+        __syncwarp();
       };
-      // S_s = Q_s K^T; K is the nkt'th K tile, in the slot of the n'th tile.  P of the stream's previous tile lies where S
-      // goes, so its product with V must be done.
+      // S_s = Q_s K^T; K is the nkt'th K tile, in the slot of the n'th tile.  P of the stream's
+      // previous tile lies where S goes, so its product with V must be done.
       auto issue_s = [&](int s, int n, bool first, bool last) {
-        if (first && !mbar_wait(bar(ctl->q_full[s]), nq[s] & 1, wc)) return false;
+        if (first && !wait(ctl->q_full[s], nq[s] & 1)) return false;
         if (!kv_wait(ctl->k_full, nkt)) return false;
-        if (steps[s] > 0 && !mbar_wait(bar(ctl->pv_done[s]), (steps[s] - 1) & 1, wc)) return false;
+        if (steps[s] > 0 && !wait(ctl->pv_done[s], (steps[s] - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t dq = sdesc_sw128(sbase + G::kOffQ + s * G::kTileBytes, 16, 1024);
-        const uint64_t dk = sdesc_sw128(sbase + G::kOffKV + (n % kStages) * G::kTileBytes, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {   // 32 bytes inside a box, boxes 16 KB apart
-          const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
-          mma_f16_ss(tmem + G::kColS + 128 * s, dq + off, dk + off, idesc_s, kk > 0);
+        if (elect_leader()) {
+          product_ss<D>(tmem + G::kColS + 128 * s, sbase + G::kOffQ + s * G::kTileBytes, slot(n));
+          mma_commit(bar(ctl->s_full[s]));
+          if (last) mma_commit(bar(ctl->q_empty[s]));   // Q may be replaced
         }
-        mma_commit(bar(ctl->s_full[s]));
-        if (last) {                              // Q may be replaced
-          mma_commit(bar(ctl->q_empty[s]));
-          ++nq[s];
-        }
+        __syncwarp();
+        nq[s] += last;
         return true;
       };
       Item x{}, y{};
       int i = next_item(a, w, blockIdx.x, &x);
       if (i < w.items) {
         for (int s = 0; ok && s < x.streams; ++s) ok = issue_s(s, nkv, true, x.t1 == x.t0 + 1);
-        if (ok) mma_commit(bar(ctl->kv_empty[nkv % kStages]));
+        if (ok) commit(ctl->kv_empty[nkv % kStages]);
         ++nkv;
         ++nkt;
       }
@@ -192,26 +190,25 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
           const bool more = t + 1 < x.t1, any = more || i2 < w.items;
           const int next_streams = more ? x.streams : i2 < w.items ? y.streams : 0;
           const int nv = nkv, nk = nkv + 1;       // V of this tile, K of the next
-          for (int s = 0; ok && s < 2; ++s) {
-            if (s < x.streams) {
-              if (t == x.t0) {                    // the previous item's O has been read
-                if (no[s] > 0 && !mbar_wait(bar(ctl->o_free[s]), (no[s] - 1) & 1, wc)) { ok = false; break; }
-                ++no[s];
-              }
-              if (!kv_wait(ctl->v_ready, nvt) || !mbar_wait(bar(ctl->p_full[s]), steps[s] & 1, wc)) { ok = false; break; }
-              tc_fence_after();
-              const uint64_t dv = sdesc_sw128(sbase + G::kOffKV + (nv % kStages) * G::kTileBytes, kBox, 1024);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)      // 16 keys: 8 columns of P, 2048 bytes of V
-                mma_f16_ts(tmem + G::kColO + D * s, tmem + G::kColS + 128 * s + 8 * kk, dv + 128 * kk, idesc_o,
-                           t > x.t0 || kk > 0);
-              mma_commit(bar(ctl->pv_done[s]));
+          for (int s = 0; s < 2; ++s) {
+            if (ok && s < x.streams) {
+              // the previous item's O has been read
+              if (t == x.t0 && no[s]++ > 0) ok = wait(ctl->o_free[s], (no[s] - 2) & 1);
+              ok = ok && kv_wait(ctl->v_ready, nvt) && wait(ctl->p_full[s], steps[s] & 1);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_leader()) {
+                product_ts<D>(tmem + G::kColO + D * s, tmem + G::kColS + 128 * s, 32, slot(nv), t > x.t0);
+                mma_commit(bar(ctl->pv_done[s]));
+                if (s == x.streams - 1) mma_commit(bar(ctl->kv_empty[nv % kStages]));
+              }
+              __syncwarp();
               ++steps[s];
             }
-            if (s == x.streams - 1) mma_commit(bar(ctl->kv_empty[nv % kStages]));
-            if (s < next_streams) ok = issue_s(s, nk, !more, more ? t + 2 == x.t1 : y.t1 == y.t0 + 1);
+            if (ok && s < next_streams) ok = issue_s(s, nk, !more, more ? t + 2 == x.t1 : y.t1 == y.t0 + 1);
           }
-          if (ok && any) mma_commit(bar(ctl->kv_empty[nk % kStages]));
+          if (ok && any) commit(ctl->kv_empty[nk % kStages]);
           nkv += 1 + any;
           nkt += any;
           ++nvt;
@@ -219,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
         x = y;
         i = i2;
       }
-      mma_commit(bar(ctl->drain));               // no product may run when tensor memory is freed
+      commit(ctl->drain);                        // no product may run when tensor memory is freed
       mbar_wait(bar(ctl->drain), 0, wc, false);
     }
   } else if (warp == 2) {
@@ -420,6 +417,7 @@ cudaError_t launch(const CrossArgs& a, int splits, const void* q, const void* k,
   if (items > INT_MAX - 4096) return cudaErrorInvalidValue;
   w.items = (int)items;
   w.padded = 0;
+  set_divisors(&w, a.H);
   float* plse = part + (size_t)splits * a.B * a.Nq * a.H * D;
   const unsigned long long limit_cycles = 2000000000ull;   // 1 s at 2 GHz
   cross_sm100_kernel<D><<<(unsigned)(items < sms ? items : sms), kThreads, smem, st>>>(tq, tk, tv, to, a, w, lse, part,
