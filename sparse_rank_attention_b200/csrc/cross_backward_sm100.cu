@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_sm100_kernel(
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   DqCtl* ctl = reinterpret_cast<DqCtl*>(base + G::kOffCtl);
   const uint32_t sbase = smem_addr(base);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   auto bar = [&](uint64_t& m) { return smem_addr(&m); };
 
   if (threadIdx.x == 0) {
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_sm100_kernel(
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
   const WaitCtl wc{&ctl->abort, g_status, kLimitCycles};
 
   if (warp == 0) {
@@ -201,83 +201,84 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_sm100_kernel(
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16(1, 128, 128, 0, 0), idesc_o = idesc_f16(1, 128, D, 0, 1);
-      int steps[2] = {0, 0}, nq[2] = {0, 0}, no[2] = {0, 0};   // tiles, items of a query tile
-      int nkv = 0, nkt = 0;                                     // K and V tiles, K tiles alone
-      bool ok = true;
-      // the columns of s = rows (smem, K-major) x tile n of the ring (K-major)
-      auto score = [&](int s, uint32_t rows, int n) {
-        tc_fence_after();
-        const uint64_t da = sdesc_sw128(rows + s * G::kTileBytes, 16, 1024);
-        const uint64_t db = sdesc_sw128(sbase + G::kOffKV + R::slot(n) * G::kTileBytes, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
-          mma_f16_ss(tmem + G::kColS + 128 * s, da + off, db + off, idesc_s, kk > 0);
-        }
-      };
-      // S of the next tile takes the columns of dS: dQ of the previous tile must be done
-      auto issue_s = [&](int s, int n, int kt, bool first, bool last) {
-        if (first && !mbar_wait(bar(ctl->q_full[s]), nq[s] & 1, wc)) return false;
-        if (!mbar_wait(bar(ctl->k_ready[R::slot(kt)]), R::full(kt), wc)) return false;
-        if (steps[s] > 0 && !mbar_wait(bar(ctl->dq_done[s]), (steps[s] - 1) & 1, wc)) return false;
-        score(s, sbase + G::kOffQ, n);
+    int steps[2] = {0, 0}, nq[2] = {0, 0}, no[2] = {0, 0};   // tiles, items of a query tile
+    int nkv = 0, nkt = 0;                                     // K and V tiles, K tiles alone
+    bool ok = true;
+    auto wait = [&](uint64_t& m, uint32_t parity) { return warp_wait(m, parity, wc); };
+    auto slot = [&](int n) { return sbase + G::kOffKV + R::slot(n) * G::kTileBytes; };
+    auto commit = [&](uint64_t& m) {
+      if (elect_leader()) mma_commit(bar(m));
+      __syncwarp();
+    };
+    // S of the next tile takes the columns of dS: dQ of the previous tile must be done
+    auto issue_s = [&](int s, int n, int kt, bool first, bool last) {
+      if (first && !wait(ctl->q_full[s], nq[s] & 1)) return false;
+      if (!wait(ctl->k_ready[R::slot(kt)], R::full(kt))) return false;
+      if (steps[s] > 0 && !wait(ctl->dq_done[s], (steps[s] - 1) & 1)) return false;
+      tc_fence_after();
+      if (elect_leader()) {
+        product_ss<D>(tmem + G::kColS + 128 * s, sbase + G::kOffQ + s * G::kTileBytes, slot(n));
         mma_commit(bar(ctl->s_full[s]));
         if (last) mma_commit(bar(ctl->q_empty[s]));
-        return true;
-      };
-      Item x{}, y{};
-      int i = next_item(a, w, blockIdx.x, &x);
-      if (i < w.items)
-        for (int s = 0; ok && s < x.streams; ++s) ok = issue_s(s, 0, 0, true, x.t1 == x.t0 + 1);
-      while (ok && i < w.items) {
-        const int i2 = next_item(a, w, i + gridDim.x, &y);
-        for (int t = x.t0; ok && t < x.t1; ++t) {
-          const bool first = t == x.t0, more = t + 1 < x.t1;
-          const int next_streams = more ? x.streams : i2 < w.items ? y.streams : 0;
-          const int n_k = nkv, n_v = nkv + 1, n_next = nkv + 2;
-          for (int s = 0; ok && s < x.streams; ++s) {           // dP = dO V^T once P has been read
-            if (first && !mbar_wait(bar(ctl->do_full[s]), nq[s] & 1, wc)) { ok = false; break; }
-            if (!mbar_wait(bar(ctl->v_full[R::slot(nkt)]), R::full(nkt), wc) ||   // V tile as many as K tile
-                !mbar_wait(bar(ctl->p_read[s]), steps[s] & 1, wc)) { ok = false; break; }
-            score(s, sbase + G::kOffDo, n_v);
-            mma_commit(bar(ctl->dp_full[s]));
-            if (!more) {
-              mma_commit(bar(ctl->do_empty[s]));
-              ++nq[s];
-            }
-          }
-          if (!ok) break;
-          mma_commit(bar(ctl->kv_empty[R::slot(n_v)]));
-          for (int s = 0; ok && s < x.streams; ++s) {           // dQ += dS K
-            if (first) {
-              if (no[s] > 0 && !mbar_wait(bar(ctl->o_free[s]), (no[s] - 1) & 1, wc)) { ok = false; break; }
-              ++no[s];
-            }
-            if (!mbar_wait(bar(ctl->ds_full[s]), steps[s] & 1, wc)) { ok = false; break; }
-            tc_fence_after();
-            const uint64_t dk = sdesc_sw128(sbase + G::kOffKV + R::slot(n_k) * G::kTileBytes, kBox, 1024);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)   // 16 keys: 8 columns of dS (its halves 64 columns apart)
-              mma_f16_ts(tmem + G::kColO + D * s, tmem + G::kColS + 128 * s + (kk >> 2) * 64 + (kk & 3) * 8,
-                         dk + 128 * kk, idesc_o, !first || kk > 0);
-            mma_commit(bar(ctl->dq_done[s]));
-            ++steps[s];
-          }
-          if (!ok) break;
-          mma_commit(bar(ctl->kv_empty[R::slot(n_k)]));
-          nkv += 2;
-          ++nkt;
-          for (int s = 0; ok && s < next_streams; ++s)
-            ok = issue_s(s, n_next, nkt, !more, more ? t + 2 == x.t1 : y.t1 == y.t0 + 1);
-        }
-        x = y;
-        i = i2;
       }
-      mma_commit(bar(ctl->drain));
-      mbar_wait(bar(ctl->drain), 0, wc, false);
+      __syncwarp();
+      return true;
+    };
+    Item x{}, y{};
+    int i = next_item(a, w, blockIdx.x, &x);
+    if (i < w.items)
+      for (int s = 0; ok && s < x.streams; ++s) ok = issue_s(s, 0, 0, true, x.t1 == x.t0 + 1);
+    while (ok && i < w.items) {
+      const int i2 = next_item(a, w, i + gridDim.x, &y);
+      for (int t = x.t0; ok && t < x.t1; ++t) {
+        const bool first = t == x.t0, more = t + 1 < x.t1;
+        const int next_streams = more ? x.streams : i2 < w.items ? y.streams : 0;
+        const int n_k = nkv, n_v = nkv + 1, n_next = nkv + 2;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {                         // dP = dO V^T once S has been read
+          if (!ok || s >= x.streams) break;
+          if (first) ok = wait(ctl->do_full[s], nq[s] & 1);
+          ok = ok && wait(ctl->v_full[R::slot(nkt)], R::full(nkt)) &&   // V tile as many as K tile
+               wait(ctl->p_read[s], steps[s] & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_leader()) {
+            product_ss<D>(tmem + G::kColS + 128 * s, sbase + G::kOffDo + s * G::kTileBytes, slot(n_v));
+            mma_commit(bar(ctl->dp_full[s]));
+            if (!more) mma_commit(bar(ctl->do_empty[s]));
+          }
+          __syncwarp();
+          nq[s] += !more;
+        }
+        if (!ok) break;
+        commit(ctl->kv_empty[R::slot(n_v)]);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {                         // dQ += dS K
+          if (!ok || s >= x.streams) break;
+          if (first && no[s]++ > 0) ok = wait(ctl->o_free[s], (no[s] - 2) & 1);
+          ok = ok && wait(ctl->ds_full[s], steps[s] & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_leader()) {
+            product_ts<D>(tmem + G::kColO + D * s, tmem + G::kColS + 128 * s, 64, slot(n_k), !first);
+            mma_commit(bar(ctl->dq_done[s]));
+          }
+          __syncwarp();
+          ++steps[s];
+        }
+        if (!ok) break;
+        commit(ctl->kv_empty[R::slot(n_k)]);
+        nkv += 2;
+        ++nkt;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (ok && s < next_streams) ok = issue_s(s, n_next, nkt, !more, more ? t + 2 == x.t1 : y.t1 == y.t0 + 1);
+      }
+      x = y;
+      i = i2;
     }
+    commit(ctl->drain);
+    mbar_wait(bar(ctl->drain), 0, wc, false);
   } else if (warp == 2) {
     // ------------------------------------------------------------ K rows that do not count (0 * NaN in dS K)
     int nkt = 0;
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) cross_dkv_sm100_kernel(
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   DkvCtl* ctl = reinterpret_cast<DkvCtl*>(base + G::kOffCtl);
   const uint32_t sbase = smem_addr(base);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   auto bar = [&](uint64_t& m) { return smem_addr(&m); };
 
   if (threadIdx.x == 0) {
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) cross_dkv_sm100_kernel(
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
   const WaitCtl wc{&ctl->abort, g_status, kLimitCycles};
 
   if (warp == 0) {
@@ -547,71 +548,66 @@ __global__ void __launch_bounds__(kDkvThreads, 1) cross_dkv_sm100_kernel(
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16(1, 128, 128, 0, 0), idesc_o = idesc_f16(1, 128, D, 0, 1);
-      int step = 0, items = 0;   // query tiles and items begun
-      bool ok = true;
-      // columns `col` = rows (smem, K-major) x tile (smem, K-major), both [128][D]
-      auto score = [&](uint32_t col, uint32_t rows, uint32_t tile) {
-        tc_fence_after();
-        const uint64_t da = sdesc_sw128(rows, 16, 1024), db = sdesc_sw128(tile, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
-          mma_f16_ss(tmem + col, da + off, db + off, idesc_s, kk > 0);
-        }
-      };
-      // columns `col` (+)= A (tensor memory, halves 64 columns apart) x tile (smem, [128 rows][D])
-      auto gather = [&](uint32_t col, uint32_t at, uint32_t tile, bool add) {
-        tc_fence_after();
-        const uint64_t db = sdesc_sw128(tile, kBox, 1024);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_f16_ts(tmem + col, tmem + at + (kk >> 2) * 64 + (kk & 3) * 8, db + 128 * kk, idesc_o, add || kk > 0);
-      };
-      // S^T of tile n of the sequence; its columns held P^T of the tile before
-      auto issue_s = [&](int n) {
-        const int s = R::slot(n);
-        if (!mbar_wait(bar(ctl->q_full[s]), R::full(n), wc)) return false;
-        if (n > 0 && !mbar_wait(bar(ctl->dv_done), (n - 1) & 1, wc)) return false;
-        score(G::kColS, sbase + G::kOffK, sbase + G::kOffQ + s * G::kTileBytes);
+    int step = 0, items = 0;   // query tiles and items begun
+    bool ok = true;
+    auto wait = [&](uint64_t& m, uint32_t parity) { return warp_wait(m, parity, wc); };
+    auto q_tile = [&](int n) { return sbase + G::kOffQ + R::slot(n) * G::kTileBytes; };
+    auto do_tile = [&](int n) { return sbase + G::kOffDo + R::slot(n) * G::kTileBytes; };
+    // S^T of tile n of the sequence; its columns held P^T of the tile before
+    auto issue_s = [&](int n) {
+      if (!wait(ctl->q_full[R::slot(n)], R::full(n))) return false;
+      if (n > 0 && !wait(ctl->dv_done, (n - 1) & 1)) return false;
+      tc_fence_after();
+      if (elect_leader()) {
+        product_ss<D>(tmem + G::kColS, sbase + G::kOffK, q_tile(n));
         mma_commit(bar(ctl->s_full));
-        return true;
-      };
-      auto issue_dp = [&](int n) {
-        const int s = R::slot(n);
-        if (!mbar_wait(bar(ctl->do_full[s]), R::full(n), wc)) return false;
-        if (n > 0 && !mbar_wait(bar(ctl->dk_done), (n - 1) & 1, wc)) return false;
-        score(G::kColP, sbase + G::kOffV, sbase + G::kOffDo + s * G::kTileBytes);
-        mma_commit(bar(ctl->dp_full));
-        return true;
-      };
-      KeyItem x{};
-      for (int i = next_key_item(a, w, blockIdx.x, &x); ok && i < w.items; i = next_key_item(a, w, i + gridDim.x, &x)) {
-        ok = mbar_wait(bar(ctl->k_full), items & 1, wc) && issue_s(step) && issue_dp(step);
-        if (ok && items > 0) ok = mbar_wait(bar(ctl->o_free), (items - 1) & 1, wc);
-        ++items;
-        for (int t = x.t0; ok && t < x.t1; ++t, ++step) {
-          const int s = R::slot(step);
-          const bool more = t + 1 < x.t1;
-          if (!mbar_wait(bar(ctl->p_full), step & 1, wc)) { ok = false; break; }
-          gather(G::kColV, G::kColS, sbase + G::kOffDo + s * G::kTileBytes, t > x.t0);
-          mma_commit(bar(ctl->dv_done));
-          mma_commit(bar(ctl->do_empty[s]));       // dP of this tile was issued before
-          if (more && !issue_s(step + 1)) { ok = false; break; }
-          if (!mbar_wait(bar(ctl->ds_full), step & 1, wc)) { ok = false; break; }
-          gather(G::kColK, G::kColP, sbase + G::kOffQ + s * G::kTileBytes, t > x.t0);
-          mma_commit(bar(ctl->dk_done));
-          mma_commit(bar(ctl->q_empty[s]));
-          if (!more)
-            mma_commit(bar(ctl->k_empty));
-          else if (!issue_dp(step + 1))
-            ok = false;
-        }
       }
-      mma_commit(bar(ctl->drain));
-      mbar_wait(bar(ctl->drain), 0, wc, false);
+      __syncwarp();
+      return true;
+    };
+    auto issue_dp = [&](int n) {
+      if (!wait(ctl->do_full[R::slot(n)], R::full(n))) return false;
+      if (n > 0 && !wait(ctl->dk_done, (n - 1) & 1)) return false;
+      tc_fence_after();
+      if (elect_leader()) {
+        product_ss<D>(tmem + G::kColP, sbase + G::kOffV, do_tile(n));
+        mma_commit(bar(ctl->dp_full));
+      }
+      __syncwarp();
+      return true;
+    };
+    KeyItem x{};
+    for (int i = next_key_item(a, w, blockIdx.x, &x); ok && i < w.items; i = next_key_item(a, w, i + gridDim.x, &x)) {
+      ok = wait(ctl->k_full, items & 1) && issue_s(step) && issue_dp(step);
+      if (ok && items > 0) ok = wait(ctl->o_free, (items - 1) & 1);
+      ++items;
+      for (int t = x.t0; ok && t < x.t1; ++t, ++step) {
+        const bool more = t + 1 < x.t1;
+        ok = wait(ctl->p_full, step & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_leader()) {
+          product_ts<D>(tmem + G::kColV, tmem + G::kColS, 64, do_tile(step), t > x.t0);
+          mma_commit(bar(ctl->dv_done));
+          mma_commit(bar(ctl->do_empty[R::slot(step)]));   // dP of this tile was issued before
+        }
+        __syncwarp();
+        ok = (!more || issue_s(step + 1)) && wait(ctl->ds_full, step & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_leader()) {
+          product_ts<D>(tmem + G::kColK, tmem + G::kColP, 64, q_tile(step), t > x.t0);
+          mma_commit(bar(ctl->dk_done));
+          mma_commit(bar(ctl->q_empty[R::slot(step)]));
+          if (!more) mma_commit(bar(ctl->k_empty));
+        }
+        __syncwarp();
+        if (more) ok = issue_dp(step + 1);
+      }
     }
+    if (elect_leader()) mma_commit(bar(ctl->drain));
+    __syncwarp();
+    mbar_wait(bar(ctl->drain), 0, wc, false);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ P^T, dS^T and results
     // Thread (row, half) has key m0 + row and the queries 64 half .. 64 half + 63 of each tile.
