@@ -202,7 +202,8 @@ __device__ __forceinline__ void load_gain(const NormRopeArgs& a, const float* __
 
 // grid (token groups, B, q | k).
 template <typename T, int E, int NORM, int ROT, int V>
-__global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int W, const T* q,
+__global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256)
+    norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int W, const T* q,
                                                         const T* k, const float* __restrict__ wq,
                                                         const float* __restrict__ wk, T* qo, T* ko) {
   constexpr int P = E / 2;
@@ -281,7 +282,8 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256) norm_rope_kernel(c
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         if (NORM != ROLA_NORM_NONE) x[j][i] = __fmul2_rn(x[j][i], gain[j][i]);
-        if (NORM == ROLA_NORM_HEAD || (NORM == ROLA_NORM_TOKEN && !ROT)) x[j][i] = __fmul2_rn(x[j][i], make_float2(f, f));
+        if (NORM == ROLA_NORM_HEAD || (NORM == ROLA_NORM_TOKEN && !ROT))
+          x[j][i] = __fmul2_rn(x[j][i], make_float2(f, f));
       }
       if (ROT) rotate<false>(cs, x[j]);
       store_pairs<E>(dst + n * so.n + j * ho, x[j]);
@@ -496,8 +498,8 @@ cudaError_t backward_v(const NormRopeArgs& a, const RowShape& s, const void* dqo
   e = cudaGetLastError();
   if (e != cudaSuccess || NORM == ROLA_NORM_NONE) return e;
   const int cols = NORM == ROLA_NORM_HEAD ? a.d : C;
-  norm_rope_dw_kernel<<<dim3((cols + 31) / 32, tensors), dim3(32, 32), 0, st>>>(part, blocks * a.B * s.G, C, cols, dwq,
-                                                                              dwk);
+  norm_rope_dw_kernel<<<dim3((cols + kSumCols - 1) / kSumCols, tensors), dim3(kSumCols, kSumRows), 0, st>>>(
+      part, blocks * a.B * s.G, C, cols, dwq, dwk);
   return cudaGetLastError();
 }
 
