@@ -277,9 +277,10 @@ ROLA_API rola_status rola_eval_exp2(const float* x, float* y, int64_t n, int mod
  * norm of q and k before the attention, the gated residual with the next norm after it, and
  * the dense cross attention to an encoder's states.  They take no plan and keep no state:
  * every call is described by its parameter struct.  Common rules: device pointers, 16-byte
- * aligned (positions, kv_len and lse: 4 bytes; key_mask: any); strides in elements, positive
- * and a multiple of 16 bytes; the strides of an axis of size one are ignored; the last axis
- * is contiguous.  Errors, streams and the absence of allocations are those of the calls above.  Types: ROLA_F32 and ROLA_BF16 (e4m3: ROLA_ERR_UNSUPPORTED).
+ * aligned (positions, kv_len and lse: 4 bytes; key_mask: any); strides in elements, at least d
+ * (modulations: at least 0) and a multiple of 16 bytes; the strides of an axis of size one are
+ * ignored; the last axis is contiguous.  Errors, streams and the absence of allocations are
+ * those of the calls above.  Types: ROLA_F32 and ROLA_BF16 (e4m3: ROLA_ERR_UNSUPPORTED).
  * Gradients have the type of the tensor they belong to; sums, statistics and the gradients
  * of parameters are fp32, and every partial sum is reduced in a fixed order.
  * ------------------------------------------------------------------------------------- */

@@ -8,7 +8,10 @@ current stream, so calls may be captured into a CUDA graph) and marshals the res
 breaks a rule raises ``RolaError`` before anything is launched.
 
 Activations are fp32 or bf16, gains, modulations and their gradients fp32.  ``stream`` is the
-stream to launch on (default: the current one); memory is then the caller's to keep alive.
+stream to run on (default: the current one): results and workspaces are allocated on it, and
+what the inputs wait for, and how long they live, is the caller's to see to, as with torch's own
+operators under ``torch.cuda.stream``.  Nothing is recorded for autograd: a training step calls
+the backwards itself.
 """
 from __future__ import annotations
 
@@ -61,6 +64,8 @@ class _Meta:
 
     def __init__(self, m):
         self.shape, self.strides, self.dtype, self.device = tuple(m[0]), m[1], m[2], m[3]
+        if max(self.shape, default=0) >= 2 ** 31:
+            raise RolaError(_UNSUPPORTED, f"a tensor of shape {list(self.shape)} has an axis past 31 bits")
 
     @property
     def contiguous(self):
@@ -70,6 +75,14 @@ class _Meta:
                 return False
             want *= n
         return True
+
+
+def _ints(where, name, values, n):
+    """`values` as n ints of 32 bits."""
+    values = tuple(values)
+    _need(len(values) == n and all(isinstance(x, int) and -2 ** 31 <= x < 2 ** 31 for x in values), where,
+          f"{name} is not {n} 32-bit integers")
+    return values
 
 
 def _m(t):
@@ -98,11 +111,17 @@ def _param(where, name, m, shape):
 
 
 def _on_device(call):
-    """Runs `call` with its first tensor's device as the current one."""
+    """Runs `call` with its first tensor's device, and the stream that it was given, as the
+    current ones: memory that torch hands out in between belongs to that stream's order."""
     @functools.wraps(call)
     def run(*args, **kw):
         first = args[0] if args else next((t for t in kw.values() if isinstance(t, torch.Tensor)), None)
         device = first.get_device() if isinstance(first, torch.Tensor) else -1
+        stream = kw.pop("stream", None)
+        if stream is not None and device >= 0:
+            _need(stream.device_index == device, "rola_" + call.__name__, "the stream is another device's")
+            with torch.cuda.stream(stream):
+                return call(*args, **kw)
         if device >= 0 and device != torch.cuda.current_device():
             with torch.cuda.device(device):
                 return call(*args, **kw)
@@ -114,8 +133,8 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+def _stream(device):
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _new(t, dtype=None):
@@ -159,9 +178,9 @@ def _rope(where, q, k, wq, wk, positions, dq_out, dk_out, norm, eps, grid, start
     p.grad_dtype = dtype if dq_out is None else _type(dq_out, where, "dq_out")
     p.norm, p.eps, p.rope_base = NORMS[norm], eps, rope_base
     p.pos = POS_GRID if rope else POS_NONE
-    p.grid_t, p.grid_h, p.grid_w = (1, 1, N) if grid is None else grid
-    p.start_t, p.start_h, p.start_w = start
-    p.rope_pairs_t, p.rope_pairs_h, p.rope_pairs_w = pairs
+    p.grid_t, p.grid_h, p.grid_w = (1, 1, N) if grid is None else _ints(where, "grid", grid, 3)
+    p.start_t, p.start_h, p.start_w = _ints(where, "start", start, 3)
+    p.rope_pairs_t, p.rope_pairs_h, p.rope_pairs_w = _ints(where, "pairs", pairs, 3)
     if positions is not None:
         _need(rope and grid is None, where, "positions come without a grid, and not with rope=False")
         _need(positions.dtype == torch.int32 and positions.contiguous
@@ -199,7 +218,7 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, *, norm="token", eps=1e-6, grid=No
                 and (t.stride() == src.stride() if t.data_ptr() == src.data_ptr() else t.is_contiguous()))), where,
                 "out is neither contiguous like q nor the input itself")
     _check(load().rola_qk_norm_rope(p[0], q.data_ptr(), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), qo.data_ptr(),
-                                    _ptr(ko), _on(stream, mq[3])), where)
+                                    _ptr(ko), _stream(mq[3])), where)
     return qo if k is None else (qo, ko)
 
 
@@ -226,7 +245,7 @@ def qk_norm_rope_backward(dq_out, dk_out=None, q=None, k=None, wq=None, wk=None,
     ws = _workspace(need, dq_out.device)
     _check(load().rola_qk_norm_rope_backward(
         p[0], dq_out.data_ptr(), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), dq.data_ptr(),
-        _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), need, _on(stream, mu[3])), where)
+        _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), need, _stream(mu[3])), where)
     return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
 
 
@@ -292,7 +311,7 @@ def gated_norm(x, branch=None, gate=None, scale=None, shift=None, weight=None, b
                   or (t is not None and t.shape == x.shape and t.dtype == dt and t.is_contiguous()
                       and t.device == x.device), where, "out is not a pair of contiguous tensors like x and y")
     _check(load().rola_gated_norm(p[0], x.data_ptr(), _ptr(branch), _ptr(gate), _ptr(scale), _ptr(shift),
-                                  _ptr(weight), _ptr(bias), _ptr(r), y.data_ptr(), _on(stream, mx[3])), where)
+                                  _ptr(weight), _ptr(bias), _ptr(r), y.data_ptr(), _stream(mx[3])), where)
     return (x if r is None else r), y
 
 
@@ -314,7 +333,7 @@ def gated_norm_backward(dy, r, dr=None, branch=None, gate=None, scale=None, weig
     ws = _workspace(need, r.device)
     _check(load().rola_gated_norm_backward(
         p[0], dy.data_ptr(), _ptr(dr), r.data_ptr(), _ptr(branch), _ptr(gate), _ptr(scale), _ptr(weight),
-        *[_ptr(t) for t in res.values()], _ptr(ws), need, _on(stream, mr[3])), where)
+        *[_ptr(t) for t in res.values()], _ptr(ws), need, _stream(mr[3])), where)
     return res
 
 
@@ -365,7 +384,7 @@ def cross_attend(q, k, v, *, kv_len=None, key_mask=None, softmax_scale=0.0, retu
     need = p[1]
     ws = _workspace(need, q.device)
     _check(load().rola_cross_attend(p[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_len), _ptr(key_mask),
-                                    out.data_ptr(), _ptr(lse), _ptr(ws), need, _on(stream, mq[3])), where)
+                                    out.data_ptr(), _ptr(lse), _ptr(ws), need, _stream(mq[3])), where)
     return (out, lse) if return_lse else out
 
 
@@ -381,7 +400,7 @@ def cross_attend_backward(dout, q, k, v, out, lse, *, kv_len=None, key_mask=None
     ws = _workspace(need, q.device)
     _check(load().rola_cross_attend_backward(
         p[0], dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), _ptr(kv_len),
-        _ptr(key_mask), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws), need, _on(stream, mq[3])), where)
+        _ptr(key_mask), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws), need, _stream(mq[3])), where)
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
