@@ -699,15 +699,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1) cross_dkv_sm100_kernel(
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
-        if (none) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        } else {
+        if (!none) {
           tmem_ld32(t_o + c, o);
           tmem_wait_ld();
         }
+        // a key that does not count has sums of 0 * dO and 0 * q, which may be NaN
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= f;
+        for (int e = 0; e < 32; ++e) o[e] = valid && !none ? o[e] * f : 0.f;
         if (m < a.Nk) {
 #pragma unroll
           for (int e = 0; e < 32; e += kVec) {

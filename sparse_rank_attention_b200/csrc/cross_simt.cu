@@ -422,10 +422,13 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dkv_kernel(
     const size_t at = (((size_t)b * a.Nk + n) * a.H + h) * D + 4 * tx;
     float* k_dst = splits == 1 ? dk + at : part + 2 * (size_t)sp_i * total + at;
     float* v_dst = splits == 1 ? dv + at : part + (2 * (size_t)sp_i + 1) * total + at;
+    // a key that does not count has sums of 0 * dO and 0 * q, which may be NaN
+    const bool counts = ok(n);
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
-      *reinterpret_cast<float4*>(k_dst + 64 * j) = ak.at(i, j, 1.f);
-      *reinterpret_cast<float4*>(v_dst + 64 * j) = av.at(i, j, 1.f);
+      *reinterpret_cast<float4*>(k_dst + 64 * j) = counts ? ak.at(i, j, 1.f) : zero;
+      *reinterpret_cast<float4*>(v_dst + 64 * j) = counts ? av.at(i, j, 1.f) : zero;
     }
   }
 }
