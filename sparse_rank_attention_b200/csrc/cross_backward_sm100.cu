@@ -40,31 +40,33 @@ constexpr unsigned long long kLimitCycles = 2000000000ull;   // 1 s at 2 GHz
 
 // ------------------------------------------------------------------ statistics
 
-// d / 8 threads per row (b, n, h); zl = lse log2 e, zd = D, both [B, H, padded].
+// zl = lse log2 e (infinity for rows without keys and rows past Nq: P = 0), zd = D = rowsum(dO * O),
+// both [B, H, padded].  d / 8 threads per row, one row each, in 32-bit indices of a sample (with
+// 64-bit divisions it was bound by them: 147 us at 32760 x 40 x 128, now 141; four rows per thread
+// take 180).
 template <int D>
-__global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant__ CrossArgs a, int padded,
+__global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant__ CrossArgs a, unsigned padded,
                                                           const __nv_bfloat16* __restrict__ dout,
                                                           const __nv_bfloat16* __restrict__ out,
                                                           const float* __restrict__ lse, float* __restrict__ zl,
                                                           float* __restrict__ zd) {
   constexpr int kPer = D / kVec;
-  const long long e = (long long)blockIdx.x * 256 + threadIdx.x, row = e / kPer;
-  const int c = (int)(e - row * kPer) * kVec, h = (int)(row % a.H);
-  const long long bn = row / a.H;
-  const int b = (int)(bn / padded), n = (int)(bn - (long long)b * padded);
+  const unsigned row = blockIdx.x * (256 / kPer) + threadIdx.x / kPer, n = row / (unsigned)a.H, h = row - n * a.H;
+  const int c = (threadIdx.x % kPer) * kVec, b = blockIdx.y;
   float s = 0.f;
-  if (b < a.B && n < a.Nq) {
+  const bool on = n < (unsigned)a.Nq;
+  if (on) {
     float u[kVec], v[kVec];
-    load8(dout + b * a.dout.b + n * a.dout.n + h * a.dout.h + c, u);
-    load8(out + (((size_t)b * a.Nq + n) * a.H + h) * D + c, v);
+    load8(dout + b * a.dout.b + (int64_t)n * a.dout.n + (int64_t)h * a.dout.h + c, u);
+    load8(out + ((size_t)b * a.Nq * a.H + row) * D + c, v);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) s = fmaf(u[i], v[i], s);
   }
 #pragma unroll
   for (int o = kPer / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (c != 0 || b >= a.B) return;
-  const size_t at = ((size_t)b * a.H + h) * padded + n;
-  const float z = n < a.Nq ? __ldg(lse + ((size_t)b * a.H + h) * a.Nq + n) : -INFINITY;
+  if (c != 0 || n >= padded) return;
+  const size_t head = (size_t)b * a.H + h, at = head * padded + n;
+  const float z = on ? __ldg(lse + head * a.Nq + n) : -INFINITY;
   zl[at] = z == -INFINITY ? INFINITY : z * 1.4426950408889634f;
   zd[at] = s;
 }
@@ -753,9 +755,9 @@ cudaError_t backward(const CrossArgs& a, int splits_q, int splits_k, const void*
   if (e != cudaSuccess) return e;
   const int padded = (int)cross_padded_rows(a.Nq), ktiles = (a.Nk + kTile - 1) / kTile;
   float *zl = stats, *zd = stats + (size_t)a.B * a.H * padded;
-  const long long threads = (long long)a.B * padded * a.H * (D / kVec);
-  cross_stats_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
-      a, padded, (const __nv_bfloat16*)dout, (const __nv_bfloat16*)out, lse, zl, zd);
+  const long long rows = (long long)padded * a.H;   // of a sample: below 2^31 + 2^17
+  cross_stats_kernel<D><<<dim3((unsigned)((rows * (D / kVec) + 255) / 256), a.B), 256, 0, st>>>(
+      a, (unsigned)padded, (const __nv_bfloat16*)dout, (const __nv_bfloat16*)out, lse, zl, zd);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
   Work w;
