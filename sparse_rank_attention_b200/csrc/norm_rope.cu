@@ -226,17 +226,22 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256)
   float2* tab = reinterpret_cast<float2*>(ring + kAhead * kRow * nt);
   const float inv = 1.f / (NORM == ROLA_NORM_TOKEN ? a.H * a.d : a.d);
   const int first = blockIdx.x * G + rg.g, step = gridDim.x * G;
-  auto fetch = [&](long long n, int s) {
-    if (n < a.N) {
+  src += first * si.n;
+  dst += first * so.n;
+  const int64_t dx = step * si.n, dout = step * so.n;
+  unsigned ahead = first;              // the next row to fetch
+  auto fetch = [&](int s) {
+    if (ahead < (unsigned)a.N) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if (h0 + j * hs < a.H)
-          fetch_piece<E>(ring + (s * kRow + j * piece_bytes<E, T>()) * nt, src + n * si.n + j * hx);
+        if (h0 + j * hs < a.H) fetch_piece<E>(ring + (s * kRow + j * piece_bytes<E, T>()) * nt, src + j * hx);
     }
     copy_commit();
+    ahead += step;
+    src += dx;
   };
 #pragma unroll
-  for (int s = 0; s < kAhead - 1; ++s) fetch(first + (long long)s * step, s);
+  for (int s = 0; s < kAhead - 1; ++s) fetch(s);
   if (ROT == kPerToken && first < a.N) turner.write(a, b, first, sh.cs[0][rg.g]);
   Walker<E> walk(a, c >> 1, first, step);
   if (ROT == kTable) {
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256)
   }
   int slot = 0, turn = 0, it = 0;
   for (long long n = first; n < a.N; n += step, ++it) {
-    fetch(n + (long long)(kAhead - 1) * step, slot == 0 ? kAhead - 1 : slot - 1);
+    fetch(slot == 0 ? kAhead - 1 : slot - 1);
     copy_wait<kAhead - 1>();
     float2 x[V][P];
     float sum = 0.f, rms[V];
@@ -286,8 +291,9 @@ __global__ void __launch_bounds__(E == 4 ? kMaxThreads : 256)
           x[j][i] = __fmul2_rn(x[j][i], make_float2(f, f));
       }
       if (ROT) rotate<false>(cs, x[j]);
-      store_pairs<E>(dst + n * so.n + j * ho, x[j]);
+      store_pairs<E>(dst + j * ho, x[j]);
     }
+    dst += dout;
     slot = slot == kAhead - 1 ? 0 : slot + 1;
     turn = next;
   }
@@ -326,20 +332,29 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rope_backward_kernel(
   float2* tab = reinterpret_cast<float2*>(ring + kAhead * kRow * nt);
   const float inv = 1.f / (NORM == ROLA_NORM_TOKEN ? C : a.d);
   const int first = blockIdx.x * G + rg.g, step = gridDim.x * G;
-  auto fetch = [&](long long n, int s) {
-    if (n < a.N) {
+  const int64_t dx = step * si.n, du = step * su.n, dout = (int64_t)step * C;
+  const int64_t ho = (int64_t)hs * a.d;
+  if (NORM != ROLA_NORM_NONE) src += first * si.n;
+  up += first * su.n;
+  dst += (int64_t)first * C;
+  unsigned ahead = first;              // the next row to fetch
+  auto fetch = [&](int s) {
+    if (ahead < (unsigned)a.N) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (h0 + j * hs < a.H) {
           uint8_t* at = ring + (s * kRow + j * (kBg + kBx)) * nt;
-          fetch_piece<E>(at, up + n * su.n + j * hu);
-          if (NORM != ROLA_NORM_NONE) fetch_piece<E>(at + kBg * nt, src + n * si.n + j * hx);
+          fetch_piece<E>(at, up + j * hu);
+          if (NORM != ROLA_NORM_NONE) fetch_piece<E>(at + kBg * nt, src + j * hx);
         }
     }
     copy_commit();
+    ahead += step;
+    up += du;
+    if (NORM != ROLA_NORM_NONE) src += dx;
   };
 #pragma unroll
-  for (int s = 0; s < kAhead - 1; ++s) fetch(first + (long long)s * step, s);
+  for (int s = 0; s < kAhead - 1; ++s) fetch(s);
   if (ROT == kPerToken && first < a.N) turner.write(a, b, first, sh.cs[0][rg.g]);
   Walker<E> walk(a, c >> 1, first, step);
   if (ROT == kTable) {
@@ -349,7 +364,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rope_backward_kernel(
   if (ROT == kPerToken) rg.sync();
   int slot = 0, turn = 0, it = 0;
   for (long long n = first; n < a.N; n += step, ++it) {
-    fetch(n + (long long)(kAhead - 1) * step, slot == 0 ? kAhead - 1 : slot - 1);
+    fetch(slot == 0 ? kAhead - 1 : slot - 1);
     copy_wait<kAhead - 1>();
     float2 cs[P];
     if (ROT == kTable) {
@@ -407,8 +422,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rope_backward_kernel(
           g[j][i] = __fmul2_rn(__ffma2_rn(xh, mm, __fmul2_rn(g[j][i], gain[j][i])), rr);
         }
       }
-      store_pairs<E>(dst + ((size_t)n * a.H + j * hs) * a.d, g[j]);
+      store_pairs<E>(dst + j * ho, g[j]);
     }
+    dst += dout;
     slot = slot == kAhead - 1 ? 0 : slot + 1;
     turn = next;
   }

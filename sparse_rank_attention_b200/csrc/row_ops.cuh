@@ -200,13 +200,16 @@ __device__ __forceinline__ void column_sum(const float* __restrict__ part, unsig
   const int lane = (y * kSumCols + threadIdx.x) & 31, warp = y / (32 / kSumCols);
   float s = 0.f;
   if (col < cols) {
-    const unsigned all = parts * fold;
-    for (unsigned i = y; i < all; i += 8 * kSumRows) {
+    const unsigned rows = kSumRows / fold, more = kSumRows - rows * fold;   // 128 values on
+    unsigned row = y / fold, f = y - row * fold;
+    while (row < parts) {
       float v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const unsigned n = i + u * kSumRows, row = n / fold;
-        v[u] = n < all ? part[row * stride + (size_t)(n - row * fold) * cols + col] : 0.f;
+        v[u] = row < parts ? part[row * stride + (size_t)f * cols + col] : 0.f;
+        row += rows;
+        f += more;
+        if (f >= fold) f -= fold, ++row;
       }
       s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
