@@ -208,15 +208,33 @@ int split_of(long long rows, int tiles, long long want, int least) {
   return (tiles + run - 1) / run;
 }
 
+// The same for fp32, whose tiles take long enough that the last round of blocks counts: of all
+// splits the one with the least rounds * (tiles of a block + its start and end) + joining, in
+// tiles' times (dq of 1000 x 257 at 12 heads of 128: 192 blocks of 5 tiles on 148 SMs 131 us, 576
+// of 1 or 2 with the sum 106; dk, dv: 240 blocks of 4 as long as 120 of 8).
+int even_split(long long rows, int tiles, int slots) {
+  int best = 1;
+  double least = 0;
+  for (int want = 1; want <= tiles && want <= 64; ++want) {
+    const int run = (tiles + want - 1) / want, s = (tiles + run - 1) / run;
+    const double rounds = (double)((rows * s + slots - 1) / slots);
+    const double cost = rounds * ((double)tiles / s + 0.4) + (s > 1 ? 0.4 + 0.1 * s : 0.0);
+    if (want == 1 || cost < least) least = cost, best = s;
+  }
+  return best;
+}
+// Resident blocks of an fp32 kernel.
+int simt_slots(int d) { return (d == 64 ? 2 : 1) * rola::kRowSMs; }
+
 struct CrossSplits {
   int keys, queries;
 };
 int tiles_of(int n, int tile) { return (n - 1) / tile + 1; }
-// Forward: blocks that share a query tile's keys (fp32: tiles of 64 x 64, two blocks an SM;
-// bf16: of 256 queries x 128 keys, one).
+// Forward: blocks that share a query tile's keys (fp32: tiles of 64 x 64; bf16: of 256 queries x
+// 128 keys, one block an SM).
 int forward_splits(const rola_cross_params& p) {
   const long long bh = (long long)p.B * p.H;
-  if (p.dtype == ROLA_F32) return split_of(bh * tiles_of(p.Nq, 64), tiles_of(p.Nk, 64), 2 * rola::kRowSMs, 2);
+  if (p.dtype == ROLA_F32) return even_split(bh * tiles_of(p.Nq, 64), tiles_of(p.Nk, 64), simt_slots(p.d));
   return split_of(bh * tiles_of(p.Nq, 256), tiles_of(p.Nk, 128), rola::kRowSMs, 4);
 }
 // Backward: the same for dq, and blocks that share a key tile's queries for dk, dv (bf16: tiles
@@ -225,7 +243,7 @@ CrossSplits backward_splits(const rola_cross_params& p) {
   const long long bh = (long long)p.B * p.H;
   if (p.dtype == ROLA_F32) {
     const int tq = tiles_of(p.Nq, 64), tk = tiles_of(p.Nk, 64);
-    return {split_of(bh * tq, tk, 2 * rola::kRowSMs, 2), split_of(bh * tk, tq, 2 * rola::kRowSMs, 2)};
+    return {even_split(bh * tq, tk, simt_slots(p.d)), even_split(bh * tk, tq, simt_slots(p.d))};
   }
   return {forward_splits(p), split_of(bh * tiles_of(p.Nk, 128), tiles_of(p.Nq, 128), 8 * rola::kRowSMs, 8)};
 }

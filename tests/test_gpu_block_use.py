@@ -192,6 +192,60 @@ def test_a_sample_without_keys_ignores_its_queries(dtype):
         L.assert_within(x[2:], *ref[n], n)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("low", [0.0, -300.0])
+def test_masks_that_empty_whole_tiles(dtype, low):
+    """Runs of invalid keys longer than a tile before, between and behind the valid ones, a
+    single valid key, and scores far below zero (their exponentials vanish without the row's
+    own maximum)."""
+    g = _gen(33)
+    B, Nq, Nk, H, d = 5, 140, 900, 2, 128
+    q, k, v = L.rand(g, B, Nq, H, d), L.rand(g, B, Nk, H, d), L.rand(g, B, Nk, H, d, dtype=dtype)
+    q[..., 0], k[..., 0] = 16.0, low * d ** 0.5 / 16                # adds `low` to every score
+    q, k, dout = q.to(dtype), k.to(dtype), L.rand(g, B, Nq, H, d, dtype=dtype)
+    mask = torch.zeros(B, Nk, dtype=torch.bool, device="cuda")
+    mask[0, 700:] = True
+    mask[1, 130:140] = mask[1, 650] = True
+    mask[2, -1] = True
+    mask[3, 0] = True
+    mask[4, :3] = mask[4, 255:257] = True
+    out, lse = rola.cross_attend(q, k, v, key_mask=mask, return_lse=True)
+    (want, oe), (wz, ze) = L.cross_ref(q, k, v, key_mask=mask)
+    L.assert_within(out, want, oe, "out")
+    L.assert_within(lse, wz, ze, "lse")
+    got = rola.cross_attend_backward(dout, q, k, v, out, lse, key_mask=mask)
+    ref = L.cross_backward_ref(dout, q, k, v, out, lse, key_mask=mask)
+    for n, x in got.items():
+        L.assert_within(x, *ref[n], n)
+
+
+@pytest.mark.parametrize("x,y", [(F32, F32), (F32, BF16), (BF16, BF16)])
+def test_gated_norm_of_a_large_mean(x, y):
+    """Rows a thousand spreads away from zero, as fp32 and as bf16 hold them."""
+    g = _gen(34)
+    r = L.rand(g, 2, 50, 640, dtype=x, shift=1000.0)
+    scale, shift = L.rand(g, 2, 2, 640, scale=0.5).unbind(1)
+    _, out = rola.gated_norm(r, None, None, scale, shift, y_dtype=y)
+    L.assert_within(out, *L.gated_norm_ref(r, None, None, scale, shift, None, None, "layer", y)[1], "y")
+    dy = L.rand(g, 2, 50, 640, dtype=y)
+    got = rola.gated_norm_backward(dy, r, None, None, None, scale)
+    for n, want in L.gated_norm_backward_ref(dy, r, None, None, None, scale, None, "layer").items():
+        L.assert_within(got[n], *want, n)
+
+
+def test_extreme_rows():
+    """Zeros (eps alone holds the norm up), the largest finite values and infinities stay in their
+    rows."""
+    x = torch.zeros(1, 4, 2, 64, device="cuda")
+    x[0, 1], x[0, 2, 0, 3], x[0, 3] = 1e18, math.inf, 1.0
+    w = torch.ones(128, device="cuda")
+    y = rola.qk_norm_rope(x, None, w, rope=False)
+    assert not y[0, 0].any() and bool(torch.isfinite(y[0, [1, 3]]).all())
+    assert torch.allclose(y[0, 1], torch.ones_like(y[0, 1])) and not bool(torch.isfinite(y[0, 2]).all())
+    z = rola.gated_norm(x.view(1, 4, 128), weight=w, norm="rms")[1].view_as(y)
+    assert torch.allclose(z[0, [0, 1, 3]], y[0, [0, 1, 3]]) and not bool(torch.isfinite(z[0, 2]).all())
+
+
 def _room(nbytes):
     if torch.cuda.mem_get_info()[0] < nbytes + (8 << 30):
         pytest.skip(f"needs {nbytes >> 30} GB free")
