@@ -22,6 +22,11 @@
 // tiles for dk, dv cannot both stay in one block's tensor memory, and adding dq up in global
 // memory would need atomics.
 //
+// Measured: 32760 queries x 512 keys, 40 heads of 128, keys masked: 1640 to 1770 us in all:
+// statistics 141 (0.67 GB, 4.8 TB/s), dq 720 (3 products), dk and dv 737 (4 products), the sums of
+// the parts 2 x 14.  As in the forward the chain of one tile bounds dq; in dk, dv two of the four
+// products wait for P^T and dS^T of the tile that they belong to.
+//
 // Every mbarrier wait is bounded, as in the forward.
 #include <climits>
 #include <cuda.h>

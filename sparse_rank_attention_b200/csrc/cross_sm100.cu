@@ -20,6 +20,14 @@
 // rows past Nq).  Blocks are persistent and walk (head, query pair) items head by head, so that
 // the blocks at work share K and V in L2.
 //
+// Measured: 75600 queries x 512 keys, 40 heads of 128 (0.79 TFLOP) 985 us back to back (804
+// TFLOP/s, 0.58 of the sustained library rate; the power limit holds the clock down) and 820 us in
+// a burst.  Neither the tensor pipe nor the exponentials nor L2 is full: what bounds it is one query
+// tile's chain S (about 1000 clocks), softmax (2300), P v (900) and the handovers between, of which
+// two run side by side.  Tried and slower: 64-key scores in two buffers (946 us in a burst), P
+// through shared memory (1000), Q an item ahead with result warps of their own (1026), spinning
+// waits (1107 up), results stored from registers (1090).
+//
 // Every mbarrier wait is bounded; when one runs out, all roles leave, copies in flight are waited
 // for and tensor memory is freed (ROLA_ERR_DEVICE_TIMEOUT in the device's status word).
 #include <climits>

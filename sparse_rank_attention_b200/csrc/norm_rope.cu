@@ -12,6 +12,13 @@
 // 2^-53 of the position), then sincospi in fp32: for a grid whose axes fit, once per block into a
 // table in shared memory (t + h + w positions instead of t * h * w); else per token, one token
 // ahead, by the first threads of the group.
+//
+// Measured, bf16 with token norm and a grid: 32760 tokens x 40 heads of 128, q and k, 223 us for
+// 1.34 GB (6.0 TB/s, 0.92 of a plain copy).  The backward of 12 heads, 154 us for 0.60 GB (0.60 of
+// a copy): there the instructions set the pace, about 490 per warp and row of 512 channels at 0.6
+// of the issue slots (unpacking three bf16 operands, the rotation, two dots, two sums over the
+// group), with 15 warps an SM at 127 registers.  Small calls (2 x 1000 tokens of 2 heads) take the
+// launch's 11 us.
 #include <cmath>
 #include <type_traits>
 
