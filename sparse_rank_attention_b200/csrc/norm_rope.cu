@@ -14,8 +14,8 @@
 // ahead, by the first threads of the group.
 //
 // Measured, bf16 with token norm and a grid: 32760 tokens x 40 heads of 128, q and k, 223 us for
-// 1.34 GB (6.0 TB/s, 0.92 of a plain copy).  The backward of 12 heads, 154 us for 0.60 GB (0.60 of
-// a copy): there the instructions set the pace, about 490 per warp and row of 512 channels at 0.6
+// 1.34 GB (6.0 TB/s, 0.92 of a plain copy).  The backward of 12 heads, 131 us for 0.60 GB (0.71 of
+// a copy): there the instructions set the pace, about 430 per warp and row of 512 channels at 0.6
 // of the issue slots (unpacking three bf16 operands, the rotation, two dots, two sums over the
 // group), with 15 warps an SM at 127 registers.  Small calls (2 x 1000 tokens of 2 heads) take the
 // launch's 11 us.
@@ -30,7 +30,8 @@ namespace {
 
 constexpr int kAhead = 3;       // token rows in flight per thread
 constexpr int kMaxGroups = 4;
-constexpr int kThreadsPerSM = 1024;
+constexpr int kThreadsPerSM = 1024;            // resident threads that a grid is sized for
+constexpr int kBackThreadsPerSM = 512;         // of the backward with a norm, at 128 registers (1024: 141 us, now 131)
 constexpr int kMaxV = 4;                       // pieces of a thread
 constexpr int kMaxThreads = 512;                // 8192 channels, pieces of 4
 constexpr int kMaxWarps = kMaxThreads / 32;
@@ -452,8 +453,8 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restr
 }
 
 // Blocks of token groups: the SMs full with the rows of both tensors and all samples.
-int token_blocks(const RowShape& s, int B, int N, int tensors) {
-  const long long fill = (long long)kRowSMs * (kThreadsPerSM / s.threads);
+int token_blocks(const RowShape& s, int B, int N, int tensors, int per_sm = kThreadsPerSM) {
+  const long long fill = (long long)kRowSMs * (per_sm / s.threads);
   long long x = (fill + (long long)B * tensors - 1) / ((long long)B * tensors);
   const long long most = (N + s.G - 1) / s.G;
   return (int)(x < most ? x : most);
@@ -468,11 +469,13 @@ cudaError_t opt_in(K kern, size_t smem) {
                            : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
-// The table pays where the blocks' copies of it hold fewer angles than their tokens.
-bool use_table(const NormRopeArgs& a, const RowShape& s, int tensors) {
+// The table pays where the blocks' copies of it hold fewer angles than their tokens (backward of
+// 32760 tokens of 12 heads on a 21 x 30 x 52 grid, 2184 entries: 141 us with it, 154 without; 40
+// heads forward: 223 and 232).
+bool use_table(const NormRopeArgs& a, int blocks) {
   if (a.rot.pos != ROLA_POS_GRID) return false;
   const long long n = table_entries(a);
-  return n <= kTableMost && n * token_blocks(s, a.B, a.N, tensors) * 2 <= (long long)a.N * (a.d / 2);
+  return n <= kTableMost && n * blocks <= (long long)a.N * (a.d / 2);
 }
 
 // Channels of a piece.
@@ -488,7 +491,8 @@ cudaError_t forward_v(const NormRopeArgs& a, const RowShape& s, const void* q, c
   cudaError_t e = opt_in(norm_rope_kernel<T, kE<T>, NORM, ROT, V>, smem);
   if (e != cudaSuccess) return e;
   norm_rope_kernel<T, kE<T>, NORM, ROT, V>
-      <<<dim3(token_blocks(s, a.B, a.N, tensors), a.B, tensors), s.threads, smem, st>>>(a, s.W, (const T*)q, (const T*)k, wq, wk, (T*)qo, (T*)ko);
+      <<<dim3(token_blocks(s, a.B, a.N, tensors), a.B, tensors), s.threads, smem, st>>>(
+          a, s.W, (const T*)q, (const T*)k, wq, wk, (T*)qo, (T*)ko);
   return cudaGetLastError();
 }
 
@@ -503,7 +507,13 @@ cudaError_t forward(const NormRopeArgs& a, const void* q, const void* k, const f
                       : forward_v<T, NORM, R, 4>(a, s, q, k, wq, wk, qo, ko, st);
   };
   if (a.rot.pos == ROLA_POS_NONE) return go(std::integral_constant<int, kNoRot>{});
-  return use_table(a, s, k ? 2 : 1) ? go(std::integral_constant<int, kTable>{}) : go(std::integral_constant<int, kPerToken>{});
+  return use_table(a, token_blocks(s, a.B, a.N, k ? 2 : 1)) ? go(std::integral_constant<int, kTable>{})
+                                                            : go(std::integral_constant<int, kPerToken>{});
+}
+
+template <int NORM>
+int back_blocks(const RowShape& s, int B, int N, int tensors) {
+  return token_blocks(s, B, N, tensors, NORM == ROLA_NORM_NONE ? kThreadsPerSM : kBackThreadsPerSM);
 }
 
 template <typename T, typename TG, int NORM, int ROT, int V>
@@ -513,7 +523,7 @@ cudaError_t backward_v(const NormRopeArgs& a, const RowShape& s, const void* dqo
   constexpr int E = kE<T, TG>;
   const size_t smem = (size_t)kAhead * V * (piece_bytes<E, TG>() + (NORM ? piece_bytes<E, T>() : 0)) * s.threads +
                       (ROT == kTable ? sizeof(float2) * table_entries(a) : 0);
-  const int tensors = dko ? 2 : 1, C = a.H * a.d, blocks = token_blocks(s, a.B, a.N, tensors);
+  const int tensors = dko ? 2 : 1, C = a.H * a.d, blocks = back_blocks<NORM>(s, a.B, a.N, tensors);
   cudaError_t e = opt_in(norm_rope_backward_kernel<T, TG, E, NORM, ROT, V>, smem);
   if (e != cudaSuccess) return e;
   norm_rope_backward_kernel<T, TG, E, NORM, ROT, V><<<dim3(blocks, a.B, tensors), s.threads, smem, st>>>(
@@ -540,7 +550,8 @@ cudaError_t backward(const NormRopeArgs& a, const void* dqo, const void* dko, co
                     : backward_v<T, TG, NORM, R, 2>(a, s, dqo, dko, q, k, wq, wk, dq, dk, dwq, dwk, part, st);
   };
   if (a.rot.pos == ROLA_POS_NONE) return go(std::integral_constant<int, kNoRot>{});
-  return use_table(a, s, dko ? 2 : 1) ? go(std::integral_constant<int, kTable>{}) : go(std::integral_constant<int, kPerToken>{});
+  return use_table(a, back_blocks<NORM>(s, a.B, a.N, dko ? 2 : 1)) ? go(std::integral_constant<int, kTable>{})
+                                                                   : go(std::integral_constant<int, kPerToken>{});
 }
 
 template <typename T, typename TG, typename... A>
@@ -562,7 +573,7 @@ int norm_rope_parts(int B, int N, int C, int tensors) {
   int most = 0;
   for (int e : {4, 8}) {               // for either type of piece
     const RowShape s = backward_shape(C, e);
-    const int n = token_blocks(s, B, N, tensors) * B * s.G;
+    const int n = back_blocks<ROLA_NORM_TOKEN>(s, B, N, tensors) * B * s.G;
     most = n > most ? n : most;
   }
   return most;
