@@ -39,7 +39,7 @@ struct GatedNormArgs {
   int64_t gate_b, gate_t, scale_b, scale_t, shift_b, shift_t;
 };
 
-void gated_norm_chunks(const rola_gated_norm_params& p, int* chunks, int* chunk);
+void gated_norm_chunks(const rola_gated_norm_params& p, bool back, int* chunks, int* chunk);
 size_t gated_norm_workspace(const rola_gated_norm_params& p);
 cudaError_t launch_gated_norm(const GatedNormArgs& a, rola_dtype xt, rola_dtype yt, rola_norm_kind kind, const void* x,
                               const void* branch, const float* gate, const float* scale, const float* shift,

@@ -22,10 +22,10 @@
 // tiles for dk, dv cannot both stay in one block's tensor memory, and adding dq up in global
 // memory would need atomics.
 //
-// Measured: 32760 queries x 512 keys, 40 heads of 128, keys masked: 1640 to 1770 us in all:
-// statistics 141 (0.67 GB, 4.8 TB/s), dq 720 (3 products), dk and dv 737 (4 products), the sums of
-// the parts 2 x 14.  As in the forward the chain of one tile bounds dq; in dk, dv two of the four
-// products wait for P^T and dS^T of the tile that they belong to.
+// Measured: 32760 queries x 512 keys, 40 heads of 128, kv_len between half and all of the keys:
+// 1640 to 1770 us: statistics 141 (0.67 GB, 4.8 TB/s), dq 720 (3 products), dk and dv 737 (4
+// products), the sums of the parts 2 x 14.  As in the forward the chain of one tile bounds dq; in
+// dk, dv two of the four products wait for P^T and dS^T of the tile that they belong to.
 //
 // Every mbarrier wait is bounded, as in the forward.
 #include <climits>
@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_sm100_kernel(
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   DqCtl* ctl = reinterpret_cast<DqCtl*>(base + G::kOffCtl);
   const uint32_t sbase = smem_addr(base);
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
+  // uniform for the compiler too
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   auto bar = [&](uint64_t& m) { return smem_addr(&m); };
 
   if (threadIdx.x == 0) {
@@ -482,7 +483,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) cross_dkv_sm100_kernel(
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   DkvCtl* ctl = reinterpret_cast<DkvCtl*>(base + G::kOffCtl);
   const uint32_t sbase = smem_addr(base);
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
+  // uniform for the compiler too
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   auto bar = [&](uint64_t& m) { return smem_addr(&m); };
 
   if (threadIdx.x == 0) {

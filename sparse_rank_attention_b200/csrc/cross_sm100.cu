@@ -59,7 +59,8 @@ struct Geo {
 };
 
 struct Ctl {
-  uint64_t q_full[2], q_empty[2], k_full[6], v_full[6], v_ready[6], kv_empty[6], s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t q_full[2], q_empty[2], k_full[6], v_full[6], v_ready[6], kv_empty[6];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t drain;
   uint32_t tmem;
   int abort;
@@ -80,7 +81,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl* ctl = reinterpret_cast<Ctl*>(base + G::kOffCtl);
   const uint32_t sbase = smem_addr(base);
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
+  // uniform for the compiler too
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   auto bar = [&](uint64_t& m) { return smem_addr(&m); };
 
   if (threadIdx.x == 0) {
@@ -363,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_sm100_kernel(
         } else if (n < a.Nq) {
           float* p = part + (((size_t)x.split * a.B + x.b) * a.Nq + n) * a.H * D + (size_t)x.h * D + c;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(p + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(p + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       if (!none) {
@@ -407,7 +410,8 @@ cudaError_t launch(const CrossArgs& a, int splits, const void* q, const void* k,
                    float* part, cudaStream_t st) {
   CUtensorMap tq, tk, tv, to;
   const rola_strides so{(int64_t)a.Nq * a.H * D, (int64_t)a.H * D, D};
-  if (!make_heads_map(&tq, q, a.B, a.Nq, a.H, D, a.q, kTile) || !make_heads_map(&tk, k, a.B, a.Nk, a.H, D, a.k, kTile) ||
+  if (!make_heads_map(&tq, q, a.B, a.Nq, a.H, D, a.q, kTile) ||
+      !make_heads_map(&tk, k, a.B, a.Nk, a.H, D, a.k, kTile) ||
       !make_heads_map(&tv, v, a.B, a.Nk, a.H, D, a.v, kTile) || !make_heads_map(&to, out, a.B, a.Nq, a.H, D, so, kTile))
     return cudaErrorInvalidValue;
   constexpr size_t smem = smem_bytes<D>();

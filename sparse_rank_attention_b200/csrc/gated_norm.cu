@@ -384,11 +384,15 @@ cudaError_t forward_v(const GatedNormArgs& a, const RowShape& s, const void* x, 
   return cudaGetLastError();
 }
 
-// Calls go with the shape's V and, where three rows of it fit, kAhead = 3, as constants.
+// Calls go with the shape's V and, where three rows of it fit, kAhead = 3, as constants (with 1
+// instead, 75600 x 5120 take 1196 us, not 858, and the backward of 32760 x 5120 741, not 571; only
+// rows of more than 4096 fp32 channels or so do not fit).
 template <int E, typename F>
 cudaError_t with_shape(const RowShape& s, int row_bytes, const F& go) {
   const bool deep = 3ull * row_bytes * s.V * s.threads <= kRing;
-  auto pick = [&](auto v) { return deep ? go(v, std::integral_constant<int, 3>{}) : go(v, std::integral_constant<int, 1>{}); };
+  auto pick = [&](auto v) {
+    return deep ? go(v, std::integral_constant<int, 3>{}) : go(v, std::integral_constant<int, 1>{});
+  };
   if constexpr (E == 4)
     if (s.V == 4) return pick(std::integral_constant<int, 4>{});
   return s.V == 2 ? pick(std::integral_constant<int, 2>{}) : pick(std::integral_constant<int, 1>{});
@@ -453,8 +457,8 @@ cudaError_t backward(const GatedNormArgs& a, rola_norm_kind kind, const void* dy
     return with_shape<E>(s, kBx * (D ? 2 : 1) + kBy * (B ? 2 : 1), [&](auto v, auto ahead) {
       constexpr int V = decltype(v)::value, kAhead = decltype(ahead)::value;
       // 320 threads (5120 channels) leave a thread 200 registers, 512 leave 128
-      return s.threads <= 320 ? backward_v<TX, TY, E, L, D, B, V, kAhead, 320>(a, s, dy, dr, r, branch, rest...)
-                              : backward_v<TX, TY, E, L, D, B, V, kAhead, kMaxThreads>(a, s, dy, dr, r, branch, rest...);
+      if (s.threads <= 320) return backward_v<TX, TY, E, L, D, B, V, kAhead, 320>(a, s, dy, dr, r, branch, rest...);
+      return backward_v<TX, TY, E, L, D, B, V, kAhead, kMaxThreads>(a, s, dy, dr, r, branch, rest...);
     });
   };
   auto pick = [&](auto layer) {
@@ -466,20 +470,21 @@ cudaError_t backward(const GatedNormArgs& a, rola_norm_kind kind, const void* dy
 
 }  // namespace
 
-// Rows that a partial sum is worth: with a group per row the sums of 2331 rows of 1000 channels
-// were as large as the rows (fp32: 13 + 11 us; with four rows a group 9 + 6), while four blocks an SM keep
-// loads enough in flight.
+// Rows that a partial sum of the backward is worth: with a group per row the sums of 2331 rows of
+// 1000 channels were as large as the rows (fp32: 13 + 11 us; with four rows a group 9 + 6), while
+// four groups an SM keep loads enough in flight.
 constexpr int kRowsPerSum = 4;
 
 // Chunks of the tokens that share a modulation row: a segment for every group of a full grid,
 // and no more (each costs a row of partial sums).
-void gated_norm_chunks(const rola_gated_norm_params& p, int* chunks, int* chunk) {
+void gated_norm_chunks(const rola_gated_norm_params& p, bool back, int* chunks, int* chunk) {
   const RowShape s = shape_of(p.C, piece_of(p.x_dtype, p.y_dtype));
   const int per = p.N / p.T;
   const long long mods = (long long)p.B * p.T;
-  const long long rows = (long long)p.B * p.N, few = rows / kRowsPerSum > 4 * kRowSMs ? rows / kRowsPerSum : 4 * kRowSMs;
+  const long long rows = (long long)p.B * p.N, sums = rows / kRowsPerSum;
+  const long long few = sums > 4 * kRowSMs ? sums : 4 * kRowSMs;
   long long groups = (long long)blocks_for(s, rows) * s.G;
-  if (groups > few) groups = few;
+  if (back && groups > few) groups = few;
   long long want = (groups + mods - 1) / mods;
   if (want > per) want = per;
   *chunk = (int)((per + want - 1) / want);
@@ -488,7 +493,7 @@ void gated_norm_chunks(const rola_gated_norm_params& p, int* chunks, int* chunk)
 
 size_t gated_norm_workspace(const rola_gated_norm_params& p) {
   int chunks, chunk;
-  gated_norm_chunks(p, &chunks, &chunk);
+  gated_norm_chunks(p, true, &chunks, &chunk);
   const long long segs = (long long)p.B * p.T * chunks;
   const RowShape s = shape_of(p.C, piece_of(p.x_dtype, p.y_dtype));
   return sizeof(float) * (size_t)p.C * ((chunks > 1 ? 3 * segs : 0) + 2 * (long long)blocks_for(s, segs) * s.G);
