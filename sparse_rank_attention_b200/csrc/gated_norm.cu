@@ -49,7 +49,8 @@ struct Cursor {
     b = mod / (unsigned)a.T;
     t = mod - b * a.T;
     n = t * a.per + ch * a.chunk;
-    n1 = min(n + a.chunk, (t + 1) * a.per);
+    const int end = (t + 1) * a.per;   // at most 2^31 - 1, which n + a.chunk may pass
+    n1 = end - n > a.chunk ? n + a.chunk : end;
   }
   // the next row; true where it opens a segment
   __device__ __forceinline__ bool next(const GatedNormArgs& a, long long segs, long long groups) {
@@ -488,7 +489,7 @@ void gated_norm_chunks(const rola_gated_norm_params& p, bool back, int* chunks, 
   long long want = (groups + mods - 1) / mods;
   if (want > per) want = per;
   *chunk = (int)((per + want - 1) / want);
-  *chunks = (per + *chunk - 1) / *chunk;
+  *chunks = (per - 1) / *chunk + 1;
 }
 
 size_t gated_norm_workspace(const rola_gated_norm_params& p) {

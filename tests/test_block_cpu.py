@@ -281,3 +281,15 @@ def test_python_calls_refuse(make, text):
     with pytest.raises(rola.RolaError) as e:
         make()
     assert text in str(e.value) and e.value.code in (INVALID, UNSUPPORTED)
+
+
+# ---------------------------------------------------------------------------- sizes at the end of their range
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_gated_norm_workspace_of_the_most_tokens(T):
+    """2^31 - 1 tokens are cut into about as many runs as half of them."""
+    most = size("rola_gated_norm_workspace_size", norm_params(B=1, N=2 ** 31 - T, C=8, T=T))
+    half = size("rola_gated_norm_workspace_size", norm_params(B=1, N=2 ** 30, C=8, T=T))
+    assert most[0] == half[0] == 0
+    assert 0 < most[1] <= 2 * half[1] and half[1] <= 2 * most[1]
