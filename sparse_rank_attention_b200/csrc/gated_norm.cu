@@ -366,11 +366,7 @@ int blocks_for(const RowShape& s, long long segs) {
   return (int)(want < most ? want : most);
 }
 
-template <typename K>
-cudaError_t opt_in(K kern, size_t smem) {
-  return smem <= 40 * 1024 ? cudaSuccess
-                           : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-}
+static_assert(kRing + sizeof(Shared) <= kMostSharedMemory, "the ring and the sums fit");
 
 template <typename TX, typename TY, int E, bool LAYER, bool BRANCH, int V, int kAhead>
 cudaError_t forward_v(const GatedNormArgs& a, const RowShape& s, const void* x, const void* branch, const float* gate,
@@ -378,7 +374,7 @@ cudaError_t forward_v(const GatedNormArgs& a, const RowShape& s, const void* x, 
                       cudaStream_t st) {
   auto* kern = gated_norm_kernel<TX, TY, E, LAYER, BRANCH, V, kAhead>;
   const size_t smem = (size_t)kAhead * V * (piece_bytes<E, TX>() + (BRANCH ? piece_bytes<E, TY>() : 0)) * s.threads;
-  const cudaError_t e = opt_in(kern, smem);
+  const cudaError_t e = allow_shared_memory<kRing>(kern, smem);
   if (e != cudaSuccess) return e;
   kern<<<blocks_for(s, (long long)a.B * a.T * a.chunks), s.threads, smem, st>>>(
       a, s.W, (const TX*)x, (const TY*)branch, gate, scale, shift, weight, bias, (TX*)r, (TY*)y);
@@ -423,7 +419,7 @@ cudaError_t backward_v(const GatedNormArgs& a, const RowShape& s, const void* dy
   auto* kern = gated_norm_backward_kernel<TX, TY, E, LAYER, DR, BRANCH, V, kAhead, kMost>;
   constexpr int kBx = piece_bytes<E, TX>(), kBy = piece_bytes<E, TY>();
   const size_t smem = (size_t)kAhead * V * (kBx * (DR ? 2 : 1) + kBy * (BRANCH ? 2 : 1)) * s.threads;
-  cudaError_t e = opt_in(kern, smem);
+  cudaError_t e = allow_shared_memory<kRing>(kern, smem);
   if (e != cudaSuccess) return e;
   const long long mods = (long long)a.B * a.T;
   const int blocks = blocks_for(s, mods * a.chunks);

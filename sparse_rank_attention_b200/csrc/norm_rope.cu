@@ -463,10 +463,10 @@ int token_blocks(const RowShape& s, int B, int N, int tensors, int per_sm = kThr
 // Backward: a thread's sums of dw stay in registers, so half as many channels per thread.
 RowShape backward_shape(int C, int E) { return row_shape(C, E, 16 / E, kMaxWarps); }
 
-template <typename K>
-cudaError_t opt_in(K kern, size_t smem) {
-  return smem <= 40 * 1024 ? cudaSuccess   // with the static part within the default
-                           : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// The most dynamic shared memory of an instance: the widest block's ring, and the largest table.
+template <int ROT>
+constexpr size_t most_smem(int row_bytes) {
+  return (size_t)kAhead * row_bytes * kMaxThreads + (ROT == kTable ? sizeof(float2) * kTableMost : 0);
 }
 
 // The table pays where the blocks' copies of it hold fewer angles than their tokens (backward of
@@ -485,10 +485,12 @@ constexpr int kE = (std::is_same_v<Ts, float> || ...) ? 4 : 8;
 template <typename T, int NORM, int ROT, int V>
 cudaError_t forward_v(const NormRopeArgs& a, const RowShape& s, const void* q, const void* k, const float* wq,
                       const float* wk, void* qo, void* ko, cudaStream_t st) {
-  const size_t smem = (size_t)kAhead * V * piece_bytes<kE<T>, T>() * s.threads +
-                      (ROT == kTable ? sizeof(float2) * table_entries(a) : 0);
+  constexpr int kRow = V * piece_bytes<kE<T>, T>();
+  constexpr size_t kMost = most_smem<ROT>(kRow);
+  static_assert(kMost + sizeof(Shared<ROT == kPerToken>) <= kMostSharedMemory, "the widest rows fit");
+  const size_t smem = (size_t)kAhead * kRow * s.threads + (ROT == kTable ? sizeof(float2) * table_entries(a) : 0);
   const int tensors = k ? 2 : 1;
-  cudaError_t e = opt_in(norm_rope_kernel<T, kE<T>, NORM, ROT, V>, smem);
+  cudaError_t e = allow_shared_memory<kMost>(norm_rope_kernel<T, kE<T>, NORM, ROT, V>, smem);
   if (e != cudaSuccess) return e;
   norm_rope_kernel<T, kE<T>, NORM, ROT, V>
       <<<dim3(token_blocks(s, a.B, a.N, tensors), a.B, tensors), s.threads, smem, st>>>(
@@ -521,10 +523,12 @@ cudaError_t backward_v(const NormRopeArgs& a, const RowShape& s, const void* dqo
                        const void* k, const float* wq, const float* wk, void* dq, void* dk, float* dwq, float* dwk,
                        float* part, cudaStream_t st) {
   constexpr int E = kE<T, TG>;
-  const size_t smem = (size_t)kAhead * V * (piece_bytes<E, TG>() + (NORM ? piece_bytes<E, T>() : 0)) * s.threads +
-                      (ROT == kTable ? sizeof(float2) * table_entries(a) : 0);
+  constexpr int kRow = V * (piece_bytes<E, TG>() + (NORM ? piece_bytes<E, T>() : 0));
+  constexpr size_t kMost = most_smem<ROT>(kRow);
+  static_assert(kMost + sizeof(Shared<ROT == kPerToken>) <= kMostSharedMemory, "the widest rows fit");
+  const size_t smem = (size_t)kAhead * kRow * s.threads + (ROT == kTable ? sizeof(float2) * table_entries(a) : 0);
   const int tensors = dko ? 2 : 1, C = a.H * a.d, blocks = back_blocks<NORM>(s, a.B, a.N, tensors);
-  cudaError_t e = opt_in(norm_rope_backward_kernel<T, TG, E, NORM, ROT, V>, smem);
+  cudaError_t e = allow_shared_memory<kMost>(norm_rope_backward_kernel<T, TG, E, NORM, ROT, V>, smem);
   if (e != cudaSuccess) return e;
   norm_rope_backward_kernel<T, TG, E, NORM, ROT, V><<<dim3(blocks, a.B, tensors), s.threads, smem, st>>>(
       a, s.W, (const TG*)dqo, (const TG*)dko, (const T*)q, (const T*)k, wq, wk, (T*)dq, (T*)dk, part);

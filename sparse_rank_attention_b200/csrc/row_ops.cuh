@@ -37,6 +37,17 @@ inline RowShape row_shape(int C, int E, int max_v, int max_warps = kMaxRowWarps)
   return s;
 }
 
+// Lets a kernel take `smem` bytes of dynamic shared memory.  The limit is state of the kernel on the
+// device, which calls from several host threads share: it is set to kMost, the most that any call
+// of this instance takes, and never to the call's own size, so that no launch finds it lowered.
+constexpr size_t kMostSharedMemory = 227 * 1024;   // of a block, with its static part
+template <size_t kMost, typename K>
+cudaError_t allow_shared_memory(K kern, size_t smem) {
+  if (smem > kMost) return cudaErrorInvalidValue;
+  if (smem <= 40 * 1024) return cudaSuccess;       // with the static part within the default
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+}
+
 // E neighbouring channels of type T, as a thread moves them: 16 bytes, or 8 where bf16 stands
 // beside fp32.  E is 8 where all tensors are bf16 and 4 where one is fp32, so that a warp's access
 // always covers whole 32-byte sectors (8 fp32 channels as two 16-byte halves would touch every

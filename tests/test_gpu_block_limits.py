@@ -1,6 +1,7 @@
 """The operators around RoLA at the edges of what they accept: as many tokens as an index of 31
 bits holds, and calls from several host threads at once."""
 import math
+import threading
 
 import pytest
 import torch
@@ -60,3 +61,68 @@ def test_gated_norm_of_the_most_tokens(T, N):
     # a thread adds its rows of a run one by one: depth <= 2^31 / 592 groups + the tree above
     tol = (2 ** 31 / 592 + 64) * L.U * torch.stack(size).sum(0)
     L.assert_within(res["dshift"][0, -1], torch.stack(parts).sum(0), tol, "dshift")
+
+
+def _two_widths(name):
+    """Two calls of one operator that run the same kernel on rows of different widths."""
+    g = _gen(61)
+
+    def rope(H, back):
+        x, w = L.rand(g, 1, 3, H, 128), L.rand(g, H * 128, shift=1.0)
+        if back:
+            return lambda: list(t for t in rola.qk_norm_rope_backward(x, None, x, None, w).values() if t is not None)
+        return lambda: [rola.qk_norm_rope(x, None, w)]
+
+    def norm(C, back):
+        x, b, m = L.rand(g, 1, 3, C), L.rand(g, 1, 3, C), L.rand(g, 1, C)
+        if back:
+            return lambda: [t for t in rola.gated_norm_backward(x, x, b, b, m).values() if t is not None]
+        return lambda: list(rola.gated_norm(x, b, m))
+
+    make = rope if name.startswith("rope") else norm
+    wide, narrow = (64, 40) if make is rope else (8192, 5136)
+    return make(wide, name.endswith("backward")), make(narrow, name.endswith("backward"))
+
+
+@pytest.mark.parametrize("name", ["rope", "rope backward", "norm", "norm backward"])
+def test_two_host_threads(name):
+    """Calls that need different amounts of shared memory of one kernel, from two threads at once:
+    neither takes from the other what its launch needs."""
+    calls = _two_widths(name)
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    start, errors = threading.Barrier(2), []
+
+    def work(call, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait(60)
+                for i in range(4000):
+                    got = call()
+                    if i % 500 == 0:
+                        torch.cuda.current_stream().synchronize()
+                        assert all(torch.equal(a, b) for a, b in zip(got, want))
+                torch.cuda.current_stream().synchronize()
+        except BaseException as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(calls, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+def test_widest_rows_beside_a_large_table():
+    """8192 fp32 channels with close to 4096 angles in shared memory: all that a block may take."""
+    g = _gen(62)
+    N, H, d, grid, pairs = 9920, 64, 128, (10, 16, 62), (1, 1, 62)
+    x, u, w = L.rand(g, 1, N, H, d), L.rand(g, 1, N, H, d), L.rand(g, H * d, shift=1.0)
+    a = L.angles(N, d, grid, pairs=pairs)
+    got = rola.qk_norm_rope(x, None, w, grid=grid, pairs=pairs)
+    L.assert_within(got, *L.norm_rope_ref(x, w, "token", a), "y")
+    got = rola.qk_norm_rope_backward(u, None, x, None, w, grid=grid, pairs=pairs)
+    dx, dxe, dw, dwe = L.norm_rope_backward_ref(u, x, w, "token", a)
+    L.assert_within(got["dq"], dx, dxe, "dq")
+    L.assert_within(got["dwq"], dw, dwe, "dwq")
