@@ -60,16 +60,39 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
-// Whether two views may share memory.  Views of equal strides that lie side by side within a
-// token or within a head (the parts of a fused projection) do not.
+struct Axis {
+  int64_t stride;
+  int n;
+};
+
+// Whether a distance of `gap` elements is less than d away from some i s0 + j s1 + l s2, each index
+// within one axis' length of zero: two views that far apart then share an element.  Axes from the
+// longest stride on; where one does not reach past the axes inside it, the answer is yes.
+bool meets(int64_t gap, const Axis* axis, int axes, int d) {
+  if (axes == 0) return gap < d && gap > -d;
+  int64_t reach = d;                   // the rest has to come closer than this
+  for (int i = 1; i < axes; ++i) reach += (axis[i].n - 1) * axis[i].stride;
+  if (axis->stride < reach) return true;
+  const int64_t low = gap / axis->stride - (gap % axis->stride < 0);
+  for (int64_t i = low; i <= low + 1; ++i)
+    if (i < axis->n && i > -axis->n && meets(gap - i * axis->stride, axis + 1, axes - 1, d)) return true;
+  return false;
+}
+
+// Whether two views may share memory.  Views of equal strides may lie inside one another's gaps (the
+// parts of a fused projection: side by side in a token, in a head, between the heads).
 bool overlaps(const View& a, const View& b) {
   if (!overlaps(a.p, a.span(), b.p, b.span())) return false;
   if (a.el != b.el || a.s.b != b.s.b || a.s.n != b.s.n || a.s.h != b.s.h) return true;
-  const int64_t gap = std::llabs((long long)(a.p - b.p)) / (int64_t)a.el;
-  const int64_t row = (int64_t)(a.H - 1) * a.s.h + a.d;
-  if (a.N > 1 && gap >= row && gap + row <= a.s.n) return false;
-  if (a.N == 1 && gap >= row) return a.B > 1 && gap + row > a.s.b;
-  return !(a.H > 1 && gap >= a.d && gap + a.d <= a.s.h);
+  Axis axis[3];
+  int axes = 0;
+  for (const Axis& x : {Axis{a.s.b, a.B}, Axis{a.s.n, a.N}, Axis{a.s.h, a.H}}) {
+    if (x.n == 1) continue;
+    int at = axes++;
+    for (; at > 0 && axis[at - 1].stride < x.stride; --at) axis[at] = axis[at - 1];
+    axis[at] = x;
+  }
+  return meets((a.p - b.p) / (int64_t)a.el, axis, axes, a.d);
 }
 bool overlaps(const View& a, const void* b, size_t nb) { return overlaps(a.p, a.span(), b, nb); }
 

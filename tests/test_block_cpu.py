@@ -293,3 +293,22 @@ def test_gated_norm_workspace_of_the_most_tokens(T):
     half = size("rola_gated_norm_workspace_size", norm_params(B=1, N=2 ** 30, C=8, T=T))
     assert most[0] == half[0] == 0
     assert 0 < most[1] <= 2 * half[1] and half[1] <= 2 * most[1]
+
+
+# ---------------------------------------------------------------------------- views that share memory
+
+
+@pytest.mark.parametrize("B,N,H,s,gap", [
+    (1, 4, 2, (0, 64, 320), 64),             # heads outside tokens: k one token on
+    (1, 4, 2, (0, 64, 320), 192),
+    (1, 5, 2, (0, 192, 128), 64),            # heads side by side, the last of a token on the next token's first
+    (2, 2, 1, (256, 192, 64), 64),           # side by side in a token, its last on the next sample's first
+    (2, 3, 2, (768, 256, 128), 768),         # k one sample on
+    (2, 3, 2, (768, 256, 128), 256 + 32),    # half a head off
+])
+def test_rope_refuses_views_in_one_another(B, N, H, s, gap):
+    """q and k in place, with elements of k on elements of q; gaps in elements."""
+    st = (ctypes.c_int64 * 3)(*s)
+    p = rope_params(B=B, N=N, H=H, grid_w=N, q=st, k=st)
+    for k in (at(0, 2 * gap), at(0, -2 * gap)):
+        assert call("rola_qk_norm_rope", p, ROPE, dict(k=k, q_out=at(0), k_out=k)) == INVALID

@@ -126,3 +126,28 @@ def test_widest_rows_beside_a_large_table():
     dx, dxe, dw, dwe = L.norm_rope_backward_ref(u, x, w, "token", a)
     L.assert_within(got["dq"], dx, dxe, "dq")
     L.assert_within(got["dwq"], dw, dwe, "dwq")
+
+
+@pytest.mark.parametrize("layout", ["token", "head", "sample", "heads first", "between heads first"])
+def test_parts_of_one_tensor_in_place(layout):
+    """q and k side by side in a token, in a head, in a sample, with the heads outside the tokens:
+    they share no element and may both be worked on in place, and what lies between stays."""
+    g = _gen(63)
+    B, N, H, d = 2, 23, 3, 64
+    shape, q, k, perm = {
+        "token": ((B, N, 3, H, d), (slice(None), slice(None), 0), (slice(None), slice(None), 2), (0, 1, 2, 3)),
+        "head": ((B, N, H, 3, d), (..., 0, slice(None)), (..., 1, slice(None)), (0, 1, 2, 3)),
+        "sample": ((B, 2, N, H, d), (slice(None), 1), (slice(None), 0), (0, 1, 2, 3)),
+        "heads first": ((B, 3, H, N, d), (slice(None), 0), (slice(None), 2), (0, 2, 1, 3)),
+        "between heads first": ((B, H, 2, N, d), (slice(None), slice(None), 1), (slice(None), slice(None), 0), (0, 2, 1, 3)),
+    }[layout]
+    x = L.rand(g, *shape, dtype=BF16)
+    wq, wk = L.rand(g, H * d, shift=1.0), L.rand(g, H * d, shift=1.0)
+    qv, kv = x[q].permute(perm), x[k].permute(perm)
+    want = rola.qk_norm_rope(qv.contiguous(), kv.contiguous(), wq, wk)
+    rest = x.clone()
+    rola.qk_norm_rope(qv, kv, wq, wk, out=(qv, kv))
+    assert torch.equal(qv, want[0]) and torch.equal(kv, want[1])
+    for part in (x, rest):
+        part[q], part[k] = 0, 0
+    assert torch.equal(x, rest)
