@@ -228,12 +228,15 @@ def qk_norm_rope_backward(dq_out, dk_out=None, q=None, k=None, wq=None, wk=None,
                           stream=None):
     """Gradients of ``qk_norm_rope`` (same options) from those of its results, which are of q's
     type or fp32 (as ``Plan.backward`` returns them).  Returns a dict: dq, dk of q's type, dwq,
-    dwk fp32; entries that do not apply are None.  q and k may be left out for norm="none"."""
+    dwk fp32; entries that do not apply are None.  For norm="none" q and k count by their type
+    alone, and one of them or both may be left out (then the results have dq_out's)."""
     where = "rola_qk_norm_rope_backward"
-    dtype = dq_out.dtype if q is None else q.dtype
     if norm != "none":
         _need(q is not None and wq is not None and (dk_out is None) == (k is None) == (wk is None), where,
               "q, k and their gains come with a norm")
+    elif q is None:
+        q = k
+    dtype = dq_out.dtype if q is None else q.dtype
     mu = _m(dq_out)
     p = _rope(where, _m(q), _m(k), _m(wq), _m(wk), _m(positions), mu, _m(dk_out), norm, eps,
               None if grid is None else tuple(grid), tuple(start), tuple(pairs), rope_base, rope)

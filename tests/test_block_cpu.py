@@ -312,3 +312,17 @@ def test_rope_refuses_views_in_one_another(B, N, H, s, gap):
     p = rope_params(B=B, N=N, H=H, grid_w=N, q=st, k=st)
     for k in (at(0, 2 * gap), at(0, -2 * gap)):
         assert call("rola_qk_norm_rope", p, ROPE, dict(k=k, q_out=at(0), k_out=k)) == INVALID
+
+
+# ---------------------------------------------------------------------------- arguments that are left out
+
+
+@pytest.mark.parametrize("make,text", [
+    (lambda: rola.qk_norm_rope_backward(Q, Q, k=Q, norm="none"), "CUDA device"),       # all but the device
+    (lambda: rola.qk_norm_rope_backward(Q.float(), Q.float(), k=Q, norm="none"), "CUDA device"),
+    (lambda: rola.qk_norm_rope_backward(Q, None, k=Q, norm="none"), "CUDA device"),
+    (lambda: rola.qk_norm_rope_backward(Q, Q, k=Q[:, :7], norm="none"), "differs from q"),
+])
+def test_rope_backward_without_q(make, text):
+    with pytest.raises(rola.RolaError, match=text):
+        make()

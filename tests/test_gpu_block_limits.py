@@ -151,3 +151,14 @@ def test_parts_of_one_tensor_in_place(layout):
     for part in (x, rest):
         part[q], part[k] = 0, 0
     assert torch.equal(x, rest)
+
+
+@pytest.mark.parametrize("dtype,grad", [(F32, F32), (BF16, BF16), (BF16, F32)])
+def test_rotation_backward_takes_its_type_from_either(dtype, grad):
+    g = _gen(64)
+    x, u, v = (L.rand(g, 2, 30, 2, 64, dtype=t) for t in (dtype, grad, grad))
+    want = rola.qk_norm_rope_backward(u, v, x, x, norm="none")
+    for how in (dict(q=x), dict(k=x), {}):
+        got = rola.qk_norm_rope_backward(u, v, **how, norm="none")
+        for n in ("dq", "dk"):
+            assert got[n].dtype == (dtype if how else grad) and torch.equal(got[n].to(dtype), want[n])
