@@ -86,7 +86,26 @@ def _ints(where, name, values, n):
 
 
 def _m(t):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+    if t is None:
+        return None
+    try:
+        return (t.shape, t.stride(), t.dtype, t.get_device())
+    except (AttributeError, TypeError, RuntimeError):
+        raise RolaError(_INVALID, f"a {type(t).__name__} in the place of a strided tensor") from None
+
+
+def _number(where, name, x):
+    try:
+        return float(x)
+    except (TypeError, ValueError, OverflowError):
+        raise RolaError(_INVALID, f"{where}: {name} is not a number") from None
+
+
+def _results(where, out, n):
+    """`out` as n tensors (or None)."""
+    _need(isinstance(out, (tuple, list)) and len(out) == n
+          and all(t is None or isinstance(t, torch.Tensor) for t in out), where, f"out is not {n} tensors")
+    return out
 
 
 def _metas(*ms):
@@ -119,7 +138,8 @@ def _on_device(call):
         device = first.get_device() if isinstance(first, torch.Tensor) else -1
         stream = kw.pop("stream", None)
         if stream is not None and device >= 0:
-            _need(stream.device_index == device, "rola_" + call.__name__, "the stream is another device's")
+            _need(isinstance(stream, torch.cuda.Stream) and stream.device_index == device, "rola_" + call.__name__,
+                  "the stream is another device's, or no stream")
             with torch.cuda.stream(stream):
                 return call(*args, **kw)
         if device >= 0 and device != torch.cuda.current_device():
@@ -159,7 +179,7 @@ def _rope(where, q, k, wq, wk, positions, dq_out, dk_out, norm, eps, grid, start
     """(params, workspace bytes) of a call; q is None for a backward without a norm."""
     q, k, wq, wk, positions, dq_out, dk_out = _metas(q, k, wq, wk, positions, dq_out, dk_out)
     first = dq_out if q is None else q
-    _need(len(first.shape) == 4, where, "q is not [B, N, H, d]")
+    _need(first is not None and len(first.shape) == 4, where, "q is not [B, N, H, d]")
     B, N, H, d = first.shape
     dtype = _type(first, where, "q")
     _need(norm in NORMS, where, f"norm {norm!r} is not one of {sorted(NORMS)}")
@@ -176,7 +196,7 @@ def _rope(where, q, k, wq, wk, positions, dq_out, dk_out, norm, eps, grid, start
     p.B, p.N, p.H, p.d = B, N, H, d
     p.dtype = dtype
     p.grad_dtype = dtype if dq_out is None else _type(dq_out, where, "dq_out")
-    p.norm, p.eps, p.rope_base = NORMS[norm], eps, rope_base
+    p.norm, p.eps, p.rope_base = NORMS[norm], _number(where, "eps", eps), _number(where, "rope_base", rope_base)
     p.pos = POS_GRID if rope else POS_NONE
     p.grid_t, p.grid_h, p.grid_w = (1, 1, N) if grid is None else _ints(where, "grid", grid, 3)
     p.start_t, p.start_h, p.start_w = _ints(where, "start", start, 3)
@@ -211,7 +231,7 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, *, norm="token", eps=1e-6, grid=No
     if out is None:
         qo, ko = _new(q), None if k is None else _new(k)
     else:
-        qo, ko = (out, None) if isinstance(out, torch.Tensor) else out
+        qo, ko = (out, None) if isinstance(out, torch.Tensor) else _results(where, out, 2)
         for t, src in ((qo, q), (ko, k)):
             _need((t is None) == (src is None) and (t is None or (
                 t.shape == q.shape and t.dtype == q.dtype and t.device == q.device
@@ -236,9 +256,10 @@ def qk_norm_rope_backward(dq_out, dk_out=None, q=None, k=None, wq=None, wk=None,
               "q, k and their gains come with a norm")
     elif q is None:
         q = k
-    dtype = dq_out.dtype if q is None else q.dtype
-    mu = _m(dq_out)
-    p = _rope(where, _m(q), _m(k), _m(wq), _m(wk), _m(positions), mu, _m(dk_out), norm, eps,
+    mu, mq = _m(dq_out), _m(q)
+    _need(mu is not None, where, "there is no dq_out")
+    dtype = mu[2] if q is None else mq[2]
+    p = _rope(where, mq, _m(k), _m(wq), _m(wk), _m(positions), mu, _m(dk_out), norm, eps,
               None if grid is None else tuple(grid), tuple(start), tuple(pairs), rope_base, rope)
     if norm == "none":                        # only their type counts
         q = k = None
@@ -267,7 +288,7 @@ def _gated(where, x, y_dtype, like_x, like_y, gate, scale, shift, weight, bias, 
     p.B, p.N, p.C = x.shape
     p.x_dtype = _type(x, where, "x")
     _need(y_dtype in _TYPES, where, f"y is {y_dtype}, not fp32 or bf16", _UNSUPPORTED)
-    p.y_dtype, p.norm, p.eps = _TYPES[y_dtype], KINDS[norm], eps
+    p.y_dtype, p.norm, p.eps = _TYPES[y_dtype], KINDS[norm], _number(where, "eps", eps)
     for t, dt in [(x, x.dtype)] + [(t, x.dtype) for t in like_x] + [(t, y_dtype) for t in like_y]:
         _need(t is None or (t.shape == x.shape and t.dtype == dt and t.contiguous), where,
               f"a tensor beside x is not a contiguous {dt} {[B, N, C]}")
@@ -300,17 +321,18 @@ def gated_norm(x, branch=None, gate=None, scale=None, shift=None, weight=None, b
     tensor will do), token n taking row n // (N / T).  norm: "layer" or "rms".  ``out``: the
     tensors (r, y); r may be x.  Returns (r, y); without a branch r is x itself."""
     where = "rola_gated_norm"
+    mx, mb = _m(x), _m(branch)
+    _need(mx is not None, where, "there is no x")
     if y_dtype is None:
-        y_dtype = x.dtype if branch is None else branch.dtype
-    mx = _m(x)
-    p = _gated(where, mx, y_dtype, (), (_m(branch),), _m(gate), _m(scale), _m(shift), _m(weight), _m(bias), norm, eps)
+        y_dtype = (mx if mb is None else mb)[2]
+    p = _gated(where, mx, y_dtype, (), (mb,), _m(gate), _m(scale), _m(shift), _m(weight), _m(bias), norm, eps)
     if out is None:
         r, y = None if branch is None else _new(x), _new(x, y_dtype)
     else:
-        r, y = out
+        r, y = _results(where, out, 2)
         r = None if branch is None else r
-        for t, dt in ((r, x.dtype), (y, y_dtype)):
-            _need((t is None and t is r and branch is None)
+        for t, dt, unused in ((r, x.dtype, branch is None), (y, y_dtype, False)):
+            _need(unused
                   or (t is not None and t.shape == x.shape and t.dtype == dt and t.is_contiguous()
                       and t.device == x.device), where, "out is not a pair of contiguous tensors like x and y")
     _check(load().rola_gated_norm(p[0], x.data_ptr(), _ptr(branch), _ptr(gate), _ptr(scale), _ptr(shift),
@@ -326,8 +348,9 @@ def gated_norm_backward(dy, r, dr=None, branch=None, gate=None, scale=None, weig
     dict: dx, dbranch, dgate, dscale, dshift (in the modulations' shape), dweight, dbias;
     entries that do not apply are None."""
     where = "rola_gated_norm_backward"
-    mr = _m(r)
-    p = _gated(where, mr, dy.dtype, (_m(dr),), (_m(dy), _m(branch)), _m(gate), _m(scale), None, _m(weight), None, norm,
+    mr, md = _m(r), _m(dy)
+    _need(mr is not None and md is not None, where, "there is no r or no dy")
+    p = _gated(where, mr, md[2], (_m(dr),), (md, _m(branch)), _m(gate), _m(scale), None, _m(weight), None, norm,
                eps)
     res = {"dx": _new(r), "dbranch": None if branch is None else _new(branch)}
     for name, t in (("dgate", gate), ("dscale", scale), ("dshift", scale), ("dweight", weight), ("dbias", weight)):
@@ -347,12 +370,13 @@ def gated_norm_backward(dy, r, dr=None, branch=None, gate=None, scale=None, weig
 def _cross(where, q, k, v, kv_len, key_mask, dout, out, lse, softmax_scale):
     """(params, workspace bytes of the forward, of the backward)."""
     q, k, v, kv_len, key_mask, dout, out, lse = _metas(q, k, v, kv_len, key_mask, dout, out, lse)
+    _need(not any(t is None for t in (q, k, v)), where, "q, k or v is missing")
     _need(len(q.shape) == 4 and len(k.shape) == 4, where, "q is not [B, Nq, H, d], or k not [B, Nk, H, d]")
     B, Nq, H, d = q.shape
     Nk = k.shape[1]
     p = RolaCrossParams()
     p.B, p.Nq, p.Nk, p.H, p.d = B, Nq, Nk, H, d
-    p.dtype, p.softmax_scale = _type(q, where, "q"), softmax_scale
+    p.dtype, p.softmax_scale = _type(q, where, "q"), _number(where, "softmax_scale", softmax_scale)
     for name, t, n in (("q", q, Nq), ("k", k, Nk), ("v", v, Nk), ("dout", dout, Nq)):
         if t is not None:
             _need(t.shape == (B, n, H, d) and t.dtype == q.dtype and (t.strides[3] == 1 or d == 1), where,
@@ -398,6 +422,7 @@ def cross_attend_backward(dout, q, k, v, out, lse, *, kv_len=None, key_mask=None
     where = "rola_cross_attend_backward"
     mq = _m(q)
     p = _cross(where, mq, _m(k), _m(v), _m(kv_len), _m(key_mask), _m(dout), _m(out), _m(lse), softmax_scale)
+    _need(dout is not None and out is not None and lse is not None, where, "dout, out or lse is missing")
     dq, dk, dv = _new(q), _new(k), _new(v)
     need = p[2]
     ws = _workspace(need, q.device)

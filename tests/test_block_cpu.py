@@ -326,3 +326,33 @@ def test_rope_refuses_views_in_one_another(B, N, H, s, gap):
 def test_rope_backward_without_q(make, text):
     with pytest.raises(rola.RolaError, match=text):
         make()
+
+
+LSE = t(2, 3, 30, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("make,text", [
+    (lambda: rola.qk_norm_rope(None, Q, W, W), "B, N, H, d"),
+    (lambda: rola.qk_norm_rope([1.0], None, W), "a list in the place"),
+    (lambda: rola.qk_norm_rope(Q, None, W.numpy()), "a ndarray in the place"),
+    (lambda: rola.qk_norm_rope(Q.to_sparse(), None, W), "channels"),
+    (lambda: rola.qk_norm_rope(Q, None, W, eps="small"), "eps is not a number"),
+    (lambda: rola.qk_norm_rope(Q, None, W, rope_base=None), "rope_base is not a number"),
+    (lambda: rola.qk_norm_rope_backward(None, Q, Q, Q, W, W), "no dq_out"),
+    (lambda: rola.qk_norm_rope_backward(None, norm="none"), "no dq_out"),
+    (lambda: rola.gated_norm(None, X), "no x"),
+    (lambda: rola.gated_norm(X, eps=None), "eps is not a number"),
+    (lambda: rola.gated_norm_backward(None, X), "no dy"),
+    (lambda: rola.gated_norm_backward(X, None), "no r"),
+    (lambda: rola.cross_attend(None, K, K), "missing"),
+    (lambda: rola.cross_attend(Q, K, None), "missing"),
+    (lambda: rola.cross_attend(Q, None, K), "missing"),
+    (lambda: rola.cross_attend(Q, K, K, softmax_scale="1"[1:]), "softmax_scale is not a number"),
+    (lambda: rola.cross_attend(Q, K, K, kv_len=50), "a int in the place"),
+    (lambda: rola.cross_attend_backward(None, Q, K, K, Q, LSE), "CUDA device|missing"),
+    (lambda: rola.cross_attend_backward(Q, Q, K, K, None, LSE), "CUDA device|missing"),
+])
+def test_python_calls_refuse_what_is_no_tensor(make, text):
+    with pytest.raises(rola.RolaError, match=text) as e:
+        make()
+    assert e.value.code == INVALID

@@ -162,3 +162,29 @@ def test_rotation_backward_takes_its_type_from_either(dtype, grad):
         got = rola.qk_norm_rope_backward(u, v, **how, norm="none")
         for n in ("dq", "dk"):
             assert got[n].dtype == (dtype if how else grad) and torch.equal(got[n].to(dtype), want[n])
+
+
+def test_calls_with_missing_parts_are_refused():
+    """Each with the rest in order: RolaError, before anything is launched."""
+    g = _gen(65)
+    q, k, w = L.rand(g, 1, 5, 2, 64), L.rand(g, 1, 7, 2, 64), torch.ones(128, device="cuda")
+    x = L.rand(g, 1, 5, 128)
+    out, lse = rola.cross_attend(q, k, k, return_lse=True)
+    y = torch.empty_like
+    for call in (lambda: rola.cross_attend_backward(None, q, k, k, out, lse),
+                 lambda: rola.cross_attend_backward(out, q, k, k, None, lse),
+                 lambda: rola.cross_attend_backward(out, q, k, k, out, None),
+                 lambda: rola.cross_attend(q, k, k, out="out"),
+                 lambda: rola.cross_attend(q, k, k, stream="stream"),
+                 lambda: rola.qk_norm_rope(q, None, w, out=(y(q),)),
+                 lambda: rola.qk_norm_rope(q, None, w, out=(y(q), y(q))),
+                 lambda: rola.qk_norm_rope(q, q, w, w, out=(y(q), None)),
+                 lambda: rola.qk_norm_rope(q, q, w, w, out=y(q)),
+                 lambda: rola.qk_norm_rope(q, None, w, out=3),
+                 lambda: rola.gated_norm(x, weight=w, out=(None, None)),
+                 lambda: rola.gated_norm(x, weight=w, out=y(x)),
+                 lambda: rola.gated_norm(x, x, weight=w, out=(None, y(x))),
+                 lambda: rola.gated_norm(x, weight=w, out=(None, y(x), None)),
+                 lambda: rola.gated_norm(x, weight=w, out=(None, "y"))):
+        with pytest.raises(rola.RolaError):
+            call()
