@@ -201,8 +201,9 @@ rola_status check(const rola_cross_params* p) {
   if (p->dtype == ROLA_FP8_E4M3) return ROLA_ERR_UNSUPPORTED;
   if (p->d != 64 && p->d != 128) return ROLA_ERR_UNSUPPORTED;
   if (p->B > kMaxGrid || p->H > 512) return ROLA_ERR_UNSUPPORTED;
-  if ((long long)p->B * p->Nq * p->H > kMaxRows || (long long)p->B * p->Nk * p->H > kMaxRows)
-    return ROLA_ERR_UNSUPPORTED;
+  // tiles end up to a pair of query tiles behind the last token
+  const long long most = kMaxRows - 255;
+  if ((long long)p->B * p->Nq * p->H > most || (long long)p->B * p->Nk * p->H > most) return ROLA_ERR_UNSUPPORTED;
   return ROLA_OK;
 }
 

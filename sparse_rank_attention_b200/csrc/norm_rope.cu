@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restr
 int token_blocks(const RowShape& s, int B, int N, int tensors, int per_sm = kThreadsPerSM) {
   const long long fill = (long long)kRowSMs * (per_sm / s.threads);
   long long x = (fill + (long long)B * tensors - 1) / ((long long)B * tensors);
-  const long long most = (N + s.G - 1) / s.G;
+  const long long most = ((long long)N + s.G - 1) / s.G;
   return (int)(x < most ? x : most);
 }
 

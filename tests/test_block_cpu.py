@@ -356,3 +356,21 @@ def test_python_calls_refuse_what_is_no_tensor(make, text):
     with pytest.raises(rola.RolaError, match=text) as e:
         make()
     assert e.value.code == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(norm=1), dict(norm=2), dict(dtype=F32, grad_dtype=F32)])
+def test_rope_workspace_of_the_most_tokens(kw):
+    """A full grid of groups either way: the partial sums do not depend on the last tokens."""
+    def need(N):
+        return size("rola_qk_norm_rope_workspace_size", rope_params(B=1, N=N, H=1, d=64, pos=0, **kw))
+    assert need(2 ** 31 - 1) == need(2 ** 30) and need(2 ** 30)[1] > 0
+
+
+@pytest.mark.parametrize("n,code", [(2 ** 31 - 1, UNSUPPORTED), (2 ** 31 - 255, UNSUPPORTED), (2 ** 31 - 256, 0)])
+def test_cross_of_the_most_tokens(n, code):
+    """Tiles that would end past 2^31 are refused."""
+    for fn in ("rola_cross_workspace_size", "rola_cross_backward_workspace_size"):
+        for dtype in (F32, BF16):
+            for kw in (dict(Nq=n, Nk=64), dict(Nq=64, Nk=n)):
+                got, need = size(fn, cross_params(B=1, H=1, dtype=dtype, **kw))
+                assert got == code and (code or need < 2 ** 50)
