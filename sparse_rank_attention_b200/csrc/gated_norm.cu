@@ -29,6 +29,7 @@ constexpr size_t kRing = 192 * 1024;  // shared memory for the rows in flight of
 constexpr int kMaxGroups = 4;
 constexpr int kMaxThreads = 512;      // 8192 channels
 constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kDeep = 3;              // rows in flight of a group, where so many fit into the ring
 
 struct Shared {
   alignas(16) float red[2][kMaxGroups][2 * kMaxWarps];
@@ -37,6 +38,9 @@ struct Shared {
 // Channels of a piece; pieces of 8 go by two, pieces of 4 by four.
 constexpr int piece_of(rola_dtype x, rola_dtype y) { return x == ROLA_F32 || y == ROLA_F32 ? 4 : 8; }
 RowShape shape_of(int C, int E) { return row_shape(C, E, 16 / E, kMaxWarps); }
+// The most threads of a block of that shape: with fewer pieces a thread than may be, rows of 8 warps
+// and more would have taken twice as many.
+constexpr int widest(int E, int V) { return V * E == 16 ? kMaxThreads : 256; }
 
 // A group's walk over its rows: the tokens of segment `seg`, then of seg + groups, ...; a segment
 // is a chunk of the tokens that share a modulation row.
@@ -61,12 +65,13 @@ struct Cursor {
   }
 };
 
-template <typename TX, typename TY, int E, bool LAYER, bool BRANCH, int V, int kAhead>
+template <typename TX, typename TY, int E, bool LAYER, bool BRANCH, int V>
 __global__ void __launch_bounds__(kMaxThreads) gated_norm_kernel(
     const __grid_constant__ GatedNormArgs a, int W, const TX* x, const TY* __restrict__ branch,
     const float* __restrict__ gate, const float* __restrict__ scale, const float* __restrict__ shift,
     const float* __restrict__ weight, const float* __restrict__ bias, TX* r, TY* __restrict__ y) {
   constexpr int kBx = piece_bytes<E, TX>(), kBb = BRANCH ? piece_bytes<E, TY>() : 0, kRow = V * (kBx + kBb);
+  constexpr int kAhead = kDeep;
   __shared__ Shared sh;
   extern __shared__ __align__(16) uint8_t ring[];   // [kAhead][V][x, branch][threads] pieces
   const RowGroup rg(W);
@@ -368,12 +373,14 @@ int blocks_for(const RowShape& s, long long segs) {
 
 static_assert(kRing + sizeof(Shared) <= kMostSharedMemory, "the ring and the sums fit");
 
-template <typename TX, typename TY, int E, bool LAYER, bool BRANCH, int V, int kAhead>
+template <typename TX, typename TY, int E, bool LAYER, bool BRANCH, int V>
 cudaError_t forward_v(const GatedNormArgs& a, const RowShape& s, const void* x, const void* branch, const float* gate,
                       const float* scale, const float* shift, const float* weight, const float* bias, void* r, void* y,
                       cudaStream_t st) {
-  auto* kern = gated_norm_kernel<TX, TY, E, LAYER, BRANCH, V, kAhead>;
-  const size_t smem = (size_t)kAhead * V * (piece_bytes<E, TX>() + (BRANCH ? piece_bytes<E, TY>() : 0)) * s.threads;
+  auto* kern = gated_norm_kernel<TX, TY, E, LAYER, BRANCH, V>;
+  constexpr int kRow = V * (piece_bytes<E, TX>() + (BRANCH ? piece_bytes<E, TY>() : 0));
+  static_assert((size_t)kDeep * kRow * widest(E, V) <= kRing, "the forward's rows always fit three times");
+  const size_t smem = (size_t)kDeep * kRow * s.threads;
   const cudaError_t e = allow_shared_memory<kRing>(kern, smem);
   if (e != cudaSuccess) return e;
   kern<<<blocks_for(s, (long long)a.B * a.T * a.chunks), s.threads, smem, st>>>(
@@ -381,18 +388,12 @@ cudaError_t forward_v(const GatedNormArgs& a, const RowShape& s, const void* x, 
   return cudaGetLastError();
 }
 
-// Calls go with the shape's V and, where three rows of it fit, kAhead = 3, as constants (with 1
-// instead, 75600 x 5120 take 1196 us, not 858, and the backward of 32760 x 5120 741, not 571; only
-// rows of more than 4096 fp32 channels or so do not fit).
+// Calls go with the shape's V as a constant.
 template <int E, typename F>
-cudaError_t with_shape(const RowShape& s, int row_bytes, const F& go) {
-  const bool deep = 3ull * row_bytes * s.V * s.threads <= kRing;
-  auto pick = [&](auto v) {
-    return deep ? go(v, std::integral_constant<int, 3>{}) : go(v, std::integral_constant<int, 1>{});
-  };
+cudaError_t with_shape(const RowShape& s, const F& go) {
   if constexpr (E == 4)
-    if (s.V == 4) return pick(std::integral_constant<int, 4>{});
-  return s.V == 2 ? pick(std::integral_constant<int, 2>{}) : pick(std::integral_constant<int, 1>{});
+    if (s.V == 4) return go(std::integral_constant<int, 4>{});
+  return s.V == 2 ? go(std::integral_constant<int, 2>{}) : go(std::integral_constant<int, 1>{});
 }
 
 template <typename TX, typename TY, typename... A>
@@ -401,8 +402,8 @@ cudaError_t forward(const GatedNormArgs& a, rola_norm_kind kind, const void* x, 
   const RowShape s = shape_of(a.C, E);
   auto go = [&](auto layer, auto with) {
     constexpr bool L = decltype(layer)::value, B = decltype(with)::value;
-    return with_shape<E>(s, piece_bytes<E, TX>() + (B ? piece_bytes<E, TY>() : 0), [&](auto v, auto ahead) {
-      return forward_v<TX, TY, E, L, B, decltype(v)::value, decltype(ahead)::value>(a, s, x, branch, rest...);
+    return with_shape<E>(s, [&](auto v) {
+      return forward_v<TX, TY, E, L, B, decltype(v)::value>(a, s, x, branch, rest...);
     });
   };
   using Y = std::true_type;
@@ -442,6 +443,11 @@ cudaError_t backward_v(const GatedNormArgs& a, const RowShape& s, const void* dy
   return cudaGetLastError();
 }
 
+// Threads of a block whose kernel may take 168 registers a thread; 512 leave 128.
+constexpr int kFewThreads = 320;
+
+// Three rows in flight where they fit into the ring, else one (with one throughout, the backward of
+// 32760 x 5120 takes 741 us, not 571; only rows of more than 4096 fp32 channels or so do not fit).
 template <typename TX, typename TY, typename... A>
 cudaError_t backward(const GatedNormArgs& a, rola_norm_kind kind, const void* dy, const void* dr, const void* r,
                      const void* branch, A... rest) {
@@ -451,11 +457,18 @@ cudaError_t backward(const GatedNormArgs& a, rola_norm_kind kind, const void* dy
   using N = std::false_type;
   auto go = [&](auto layer, auto add, auto with) {
     constexpr bool L = decltype(layer)::value, D = decltype(add)::value, B = decltype(with)::value;
-    return with_shape<E>(s, kBx * (D ? 2 : 1) + kBy * (B ? 2 : 1), [&](auto v, auto ahead) {
-      constexpr int V = decltype(v)::value, kAhead = decltype(ahead)::value;
-      // 320 threads (5120 channels) leave a thread 200 registers, 512 leave 128
-      if (s.threads <= 320) return backward_v<TX, TY, E, L, D, B, V, kAhead, 320>(a, s, dy, dr, r, branch, rest...);
-      return backward_v<TX, TY, E, L, D, B, V, kAhead, kMaxThreads>(a, s, dy, dr, r, branch, rest...);
+    return with_shape<E>(s, [&](auto v) {
+      constexpr int V = decltype(v)::value, kMost = widest(E, V);
+      constexpr size_t kRows = (size_t)kDeep * V * (kBx * (D ? 2 : 1) + kBy * (B ? 2 : 1));   // bytes of a thread
+      const bool deep = kRows * s.threads <= kRing, few = s.threads <= kFewThreads;
+      // of the four combinations those that some width takes
+      if constexpr (kMost > kFewThreads && kRows * (kFewThreads + 32) <= kRing)
+        if (deep && !few) return backward_v<TX, TY, E, L, D, B, V, kDeep, kMost>(a, s, dy, dr, r, branch, rest...);
+      if constexpr (kMost > kFewThreads && kRows * kMost > kRing)
+        if (!deep && !few) return backward_v<TX, TY, E, L, D, B, V, 1, kMost>(a, s, dy, dr, r, branch, rest...);
+      if constexpr (kRows * (kMost < kFewThreads ? kMost : kFewThreads) > kRing)
+        if (!deep && few) return backward_v<TX, TY, E, L, D, B, V, 1, kFewThreads>(a, s, dy, dr, r, branch, rest...);
+      return backward_v<TX, TY, E, L, D, B, V, kDeep, kFewThreads>(a, s, dy, dr, r, branch, rest...);
     });
   };
   auto pick = [&](auto layer) {

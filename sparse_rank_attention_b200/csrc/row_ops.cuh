@@ -15,7 +15,6 @@ namespace rola {
 
 constexpr int kVec = 8;              // channels of a vector
 constexpr int kMaxRowChannels = 8192;
-constexpr int kMaxRowWarps = 8;      // of a group: 8192 channels at V = 4
 constexpr int kRowSMs = 148;
 
 // Threads of a row: W warps with V pieces each.  More pieces per thread mean fewer threads to
@@ -25,7 +24,7 @@ constexpr int kRowSMs = 148;
 struct RowShape {
   int V, W, G, threads;   // G groups in a block
 };
-inline RowShape row_shape(int C, int E, int max_v, int max_warps = kMaxRowWarps) {
+inline RowShape row_shape(int C, int E, int max_v, int max_warps) {
   const int pieces = C / E;
   RowShape s{1, (pieces + 31) / 32, 1, 0};
   for (int v = 2; v <= max_v; v *= 2) {

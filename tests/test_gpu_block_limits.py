@@ -188,3 +188,23 @@ def test_calls_with_missing_parts_are_refused():
                  lambda: rola.gated_norm(x, weight=w, out=(None, "y"))):
         with pytest.raises(rola.RolaError):
             call()
+
+
+@pytest.mark.parametrize("x,y", [(F32, F32), (F32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("C", [888, 904, 1784, 1800, 4096, 4104, 5120, 5128, 6144, 6152, 8184, 8192])
+def test_gated_norm_on_both_sides_of_every_variant(C, x, y):
+    """Widths where the pieces of a thread, the rows in flight or a block's threads change."""
+    g = _gen(66)
+    B, N = 2, 7
+    r, dr, branch = L.rand(g, B, N, C, dtype=x), L.rand(g, B, N, C, dtype=x), L.rand(g, B, N, C, dtype=y)
+    dy, (gate, scale, shift) = L.rand(g, B, N, C, dtype=y), L.rand(g, B, 3, C, scale=0.5).unbind(1)
+    for b in (None, branch):
+        gb = None if b is None else gate
+        wr, wy = L.gated_norm_ref(r, b, gb, scale, shift, None, None, "layer", y)
+        res = rola.gated_norm(r, b, gb, scale, shift, y_dtype=y)
+        L.assert_within(res[0], *wr, "r")
+        L.assert_within(res[1], *wy, "y")
+        for up in (None, dr):
+            got = rola.gated_norm_backward(dy, r, up, b, gb, scale)
+            for n, want in L.gated_norm_backward_ref(dy, r, up, b, gb, scale, None, "layer").items():
+                L.assert_within(got[n], *want, n)
