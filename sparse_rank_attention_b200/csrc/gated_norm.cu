@@ -443,9 +443,11 @@ cudaError_t backward_v(const GatedNormArgs& a, const RowShape& s, const void* dy
   return cudaGetLastError();
 }
 
-// Threads of a block whose kernel may take 168 registers a thread; 512 leave 128.
-constexpr int kFewThreads = 320;
-
+// A block is compiled for up to 320, 384 or 512 threads.  384 leave a thread 168 registers and 512 leave
+// 128, at which the wide rows spill: 27300 rows of 6144 channels with dr and branch, 384 threads, take
+// 639 us (x fp32, branch bf16) and 403 (bf16) compiled for 384, 1020 and 750 for 512.  320 leave 168 as
+// well, but give other code: compiled for 384 instead, 2048 bf16 channels take 369 us, not 352, and
+// 2048 of fp32 and bf16 without dr and branch 366, not 337.
 // Three rows in flight where they fit into the ring, else one (with one throughout, the backward of
 // 32760 x 5120 takes 741 us, not 571; only rows of more than 4096 fp32 channels or so do not fit).
 template <typename TX, typename TY, typename... A>
@@ -460,15 +462,23 @@ cudaError_t backward(const GatedNormArgs& a, rola_norm_kind kind, const void* dy
     return with_shape<E>(s, [&](auto v) {
       constexpr int V = decltype(v)::value, kMost = widest(E, V);
       constexpr size_t kRows = (size_t)kDeep * V * (kBx * (D ? 2 : 1) + kBy * (B ? 2 : 1));   // bytes of a thread
-      const bool deep = kRows * s.threads <= kRing, few = s.threads <= kFewThreads;
-      // of the four combinations those that some width takes
-      if constexpr (kMost > kFewThreads && kRows * (kFewThreads + 32) <= kRing)
-        if (deep && !few) return backward_v<TX, TY, E, L, D, B, V, kDeep, kMost>(a, s, dy, dr, r, branch, rest...);
-      if constexpr (kMost > kFewThreads && kRows * kMost > kRing)
-        if (!deep && !few) return backward_v<TX, TY, E, L, D, B, V, 1, kMost>(a, s, dy, dr, r, branch, rest...);
-      if constexpr (kRows * (kMost < kFewThreads ? kMost : kFewThreads) > kRing)
-        if (!deep && few) return backward_v<TX, TY, E, L, D, B, V, 1, kFewThreads>(a, s, dy, dr, r, branch, rest...);
-      return backward_v<TX, TY, E, L, D, B, V, kDeep, kFewThreads>(a, s, dy, dr, r, branch, rest...);
+      const bool deep = kRows * s.threads <= kRing;
+      // blocks of kLeast to kBound threads: with three rows in flight, or one, where some width takes it
+      auto most = [&](auto least, auto bound) {
+        constexpr int kLeast = decltype(least)::value, kBound = decltype(bound)::value;
+        constexpr int kWidest = kBound < kMost ? kBound : kMost;
+        if constexpr (kRows * kWidest > kRing)
+          if (!deep) return backward_v<TX, TY, E, L, D, B, V, 1, kBound>(a, s, dy, dr, r, branch, rest...);
+        if constexpr (kRows * kLeast <= kRing)
+          return backward_v<TX, TY, E, L, D, B, V, kDeep, kBound>(a, s, dy, dr, r, branch, rest...);
+        else
+          return cudaErrorInvalidValue;
+      };
+      if constexpr (kMost > 320) {
+        if (s.threads > 384) return most(std::integral_constant<int, 416>{}, std::integral_constant<int, kMost>{});
+        if (s.threads > 320) return most(std::integral_constant<int, 352>{}, std::integral_constant<int, 384>{});
+      }
+      return most(std::integral_constant<int, 32>{}, std::integral_constant<int, 320>{});
     });
   };
   auto pick = [&](auto layer) {
