@@ -223,7 +223,8 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, *, norm="token", eps=1e-6, grid=No
     Positions: ``grid`` (t, h, w) for tokens in that order, moved by ``start`` (tokens past the
     grid are not turned; default a 1D grid), or ``positions`` int32 [N, 3] or [B, N, 3]; with
     ``rope=False`` the norm alone.  ``out``: the two results' tensors, contiguous, or q and k
-    themselves.  Returns (q_out, k_out), or q_out alone without k."""
+    themselves.  Returns (q_out, k_out), or q_out alone without k.  Nothing is recorded for
+    autograd: ``qk_norm_rope_backward`` gives the gradients."""
     where = "rola_qk_norm_rope"
     mq = _m(q)
     p = _rope(where, mq, _m(k), _m(wq), _m(wk), _m(positions), None, None, norm, eps,
@@ -319,7 +320,8 @@ def gated_norm(x, branch=None, gate=None, scale=None, shift=None, weight=None, b
     x [B, N, C]; branch and y in ``y_dtype`` (default: branch's type, else x's; bf16 beside an
     fp32 x is fine).  gate, scale, shift: fp32 [B, C] or [B, T, C] (views of one modulation
     tensor will do), token n taking row n // (N / T).  norm: "layer" or "rms".  ``out``: the
-    tensors (r, y); r may be x.  Returns (r, y); without a branch r is x itself."""
+    tensors (r, y); r may be x.  Returns (r, y); without a branch r is x itself.  Nothing is
+    recorded for autograd: ``gated_norm_backward`` gives the gradients."""
     where = "rola_gated_norm"
     mx, mb = _m(x), _m(branch)
     _need(mx is not None, where, "there is no x")
@@ -400,7 +402,9 @@ def cross_attend(q, k, v, *, kv_len=None, key_mask=None, softmax_scale=0.0, retu
     """Dense softmax attention of q [B, Nq, H, d] to k, v [B, Nk, H, d] (any token, head and
     batch strides).  Key m counts when m < kv_len[b] (int32 [B]) and key_mask[b, m] (bool or
     uint8 [B, Nk]); a sample without keys gives zeros.  softmax_scale 0: 1/sqrt(d).  Returns
-    out [B, Nq, H, d], with ``return_lse`` also the log sum of exponentials fp32 [B, H, Nq]."""
+    out [B, Nq, H, d], with ``return_lse`` also the log sum of exponentials fp32 [B, H, Nq].
+    In bf16 the probabilities are rounded to bf16 before their product with v (sums are fp32).
+    Nothing is recorded for autograd: ``cross_attend_backward`` gives the gradients."""
     where = "rola_cross_attend"
     mq = _m(q)
     p = _cross(where, mq, _m(k), _m(v), _m(kv_len), _m(key_mask), None, _m(out), None, softmax_scale)
@@ -418,7 +422,8 @@ def cross_attend(q, k, v, *, kv_len=None, key_mask=None, softmax_scale=0.0, retu
 @_on_device
 def cross_attend_backward(dout, q, k, v, out, lse, *, kv_len=None, key_mask=None, softmax_scale=0.0, stream=None):
     """Gradients of ``cross_attend`` from dout, with the forward's inputs, out and lse.  Returns
-    a dict: dq, dk, dv, contiguous and of q's type."""
+    a dict: dq, dk, dv, contiguous and of q's type.  In bf16 the probabilities and their gradients
+    are rounded to bf16 before their products (sums are fp32)."""
     where = "rola_cross_attend_backward"
     mq = _m(q)
     p = _cross(where, mq, _m(k), _m(v), _m(kv_len), _m(key_mask), _m(dout), _m(out), _m(lse), softmax_scale)

@@ -208,3 +208,28 @@ def test_gated_norm_on_both_sides_of_every_variant(C, x, y):
             got = rola.gated_norm_backward(dy, r, up, b, gb, scale)
             for n, want in L.gated_norm_backward_ref(dy, r, up, b, gb, scale, None, "layer").items():
                 L.assert_within(got[n], *want, n)
+
+
+@pytest.mark.parametrize("Nq,Nk,d", [(500, 512, 128), (700, 333, 64)])
+def test_what_bf16_probabilities_cost(Nq, Nk, d):
+    """The rms error that rola.h states.  A rounding to bf16 is uniform within 2^-8 / m of a value
+    with mantissa m; for mantissas spread evenly over their logarithm E[1 / m^2] = 3 / (8 ln 2), so
+    its rms is e = 2^-8 (1 / 3 * 3 / (8 ln 2))^(1/2) = 0.00166 of the values'.  Against v and dout
+    of independent signs the roundings of P (and of dS) add up like the terms that they round:
+    another e.  dq and dk see the rounding of `out` in D too, which is no larger than dS: at most
+    three e's in squares.  A tenth is left for mantissas that are not spread so."""
+    e = 2.0 ** -8 * (1 / (8 * math.log(2))) ** 0.5
+    g = _gen(67)
+    q, k = (L.rand(g, 2, n, 4, d, dtype=BF16, scale=s) for n, s in ((Nq, 1.5), (Nk, 1.2)))
+    v, dout = L.rand(g, 2, Nk, 4, d, dtype=BF16), L.rand(g, 2, Nq, 4, d, dtype=BF16)
+
+    def off(got, want):
+        return float((got.double() - want).norm() / want.norm())
+
+    out, lse = rola.cross_attend(q, k, v, return_lse=True)
+    (want, _), (z, _) = L.cross_ref(q, k, v)
+    assert off(out, want) <= 1.1 * 2 ** 0.5 * e
+    got = rola.cross_attend_backward(dout, q, k, v, out, lse)
+    ref = L.cross_backward_ref(dout, q, k, v, want, z)
+    for n, squares in (("dq", 3), ("dk", 3), ("dv", 2)):
+        assert off(got[n], ref[n][0]) <= 1.1 * squares ** 0.5 * e, n
