@@ -283,6 +283,10 @@ ROLA_API rola_status rola_eval_exp2(const float* x, float* y, int64_t n, int mod
  * those of the calls above.  Types: ROLA_F32 and ROLA_BF16 (e4m3: ROLA_ERR_UNSUPPORTED).
  * Gradients have the type of the tensor they belong to; sums, statistics and the gradients
  * of parameters are fp32, and every partial sum is reduced in a fixed order.
+ * Every size is at least 1 (a cross attention of no keys: kv_len 0); B*N is at most 2^31 - 1, in
+ * the cross attention B*Nq*H and B*Nk*H at most 2^31 - 256.  The norms' sums of squares are fp32: a
+ * row whose sum passes the largest fp32 (rms above 1.8e19 / sqrt(channels)) is out of their range,
+ * and its results are zeros or not finite; other rows do not see it, sums over rows do.
  * ------------------------------------------------------------------------------------- */
 
 /* Element strides of a [B, N, H, d] tensor whose channels are contiguous. */

@@ -233,3 +233,27 @@ def test_what_bf16_probabilities_cost(Nq, Nk, d):
     ref = L.cross_backward_ref(dout, q, k, v, want, z)
     for n, squares in (("dq", 3), ("dk", 3), ("dv", 2)):
         assert off(got[n], ref[n][0]) <= 1.1 * squares ** 0.5 * e, n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_past_the_range_of_the_sums(dtype):
+    """Up to a sum of squares of 0.9 of the largest fp32 rows come out as any others; past it they
+    are zeros or not finite, and the rows beside them keep their bits."""
+    g = _gen(68)
+    N, H, d = 6, 4, 128
+    top, big = torch.finfo(F32).max, torch.finfo(dtype).max
+    x, w = L.rand(g, 1, N, H, d, dtype=dtype), L.rand(g, H * d, scale=0.1, shift=1.0)
+    x[0, 1] *= (0.9 * top / float(x[0, 1].double().square().sum())) ** 0.5
+    x[0, 3], x[0, 5] = 1e19, big
+    u = L.rand(g, 1, N, H, d, dtype=dtype)
+    rest = x.clone()
+    rest[0, [3, 5]] = 1.0
+    flat, flat_rest, flat_u = (t.view(1, N, H * d) for t in (x, rest, u))
+    for f in (lambda x, y: rola.qk_norm_rope(x, None, w), lambda x, y: rola.gated_norm(y, weight=w, norm="rms")[1],
+              lambda x, y: rola.qk_norm_rope_backward(u, None, x, None, w)["dq"],
+              lambda x, y: rola.gated_norm_backward(flat_u, y, weight=w, norm="rms")["dx"]):
+        got, want = f(x, flat)[0], f(rest, flat_rest)[0]
+        assert torch.equal(got[[0, 1, 2, 4]], want[[0, 1, 2, 4]])
+        assert not bool((torch.isfinite(got[[3, 5]]) & (got[[3, 5]] != 0)).any())
+    y, bound = L.norm_rope_ref(x, w, "token", L.angles(N, d))
+    L.assert_within(rola.qk_norm_rope(x, None, w)[:, :3], y[:, :3], bound[:, :3], "y")
