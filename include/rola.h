@@ -396,7 +396,8 @@ ROLA_API rola_status rola_gated_norm_backward(const rola_gated_norm_params* p, c
  * a sample without a valid key gives out = 0, lse = -inf and zero gradients.
  * ROLA_BF16: exp(S - max) and, in the backward, P and dS are rounded to bf16 where they enter the
  * products with v, dout, q and k; scores, statistics and sums are fp32.  Against 64 bits the rms
- * error is 0.0022 of the result (gradients 0.0025), of which the results' own rounding makes 0.0017.
+ * error is 0.0022 to 0.0024 of the result (gradients 0.0025), of which the results' own rounding
+ * makes 0.0017.
  * q [B, Nq, H, d], k, v [B, Nk, H, d] with the strides given (d 64 | 128).  out contiguous;
  * lse [B, H, Nq] fp32, or null in the forward. */
 typedef struct {

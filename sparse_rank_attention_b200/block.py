@@ -217,7 +217,8 @@ def _rope(where, q, k, wq, wk, positions, dq_out, dk_out, norm, eps, grid, start
 @_on_device
 def qk_norm_rope(q, k=None, wq=None, wk=None, *, norm="token", eps=1e-6, grid=None, start=(0, 0, 0), positions=None,
                  pairs=(0, 0, 0), rope_base=10000.0, rope=True, out=None, stream=None):
-    """RMS norm and rotary positions of q and k [B, N, H, d] (any token, head and batch strides).
+    """RMS norm and rotary positions of q and k [B, N, H, d] (token, head and batch strides of whole
+    16 bytes, d at least).
 
     norm: "token" (over H*d channels, gains wq, wk [H*d]), "head" (over d, gains [d]) or "none".
     Positions: ``grid`` (t, h, w) for tokens in that order, moved by ``start`` (tokens past the
@@ -399,8 +400,8 @@ def _cross(where, q, k, v, kv_len, key_mask, dout, out, lse, softmax_scale):
 
 @_on_device
 def cross_attend(q, k, v, *, kv_len=None, key_mask=None, softmax_scale=0.0, return_lse=False, out=None, stream=None):
-    """Dense softmax attention of q [B, Nq, H, d] to k, v [B, Nk, H, d] (any token, head and
-    batch strides).  Key m counts when m < kv_len[b] (int32 [B]) and key_mask[b, m] (bool or
+    """Dense softmax attention of q [B, Nq, H, d] to k, v [B, Nk, H, d] (token, head and batch
+    strides of whole 16 bytes, d at least).  Key m counts when m < kv_len[b] (int32 [B]) and key_mask[b, m] (bool or
     uint8 [B, Nk]); a sample without keys gives zeros.  softmax_scale 0: 1/sqrt(d).  Returns
     out [B, Nq, H, d], with ``return_lse`` also the log sum of exponentials fp32 [B, H, Nq].
     In bf16 the probabilities are rounded to bf16 before their product with v (sums are fp32).

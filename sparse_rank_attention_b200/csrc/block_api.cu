@@ -222,7 +222,9 @@ CrossArgs args_of(const rola_cross_params& p, const int32_t* kv_len, const uint8
 
 // Blocks that share the long axis (`tiles` tiles) of one of `rows` independent tiles: `want`
 // blocks in all, each with `least` tiles at least (joining the parts costs a launch and the
-// parts' traffic; for one query and 512 keys, 4 tiles, one block a head takes 14 us, as do more).
+// parts' traffic).  Forward of 12 heads of 128, in one part, as chosen, in more: one query
+// to 2000 keys 36, 16 and 15 us, to 8192 keys 130, 24 and 35; 200 queries to 8192 keys 139, 35 and
+// 64, at 40 heads 141, 70 and 98.  Under 8 tiles (2 x 1 query, 512 keys) one part takes 12 us, four 11.
 int split_of(long long rows, int tiles, long long want, int least) {
   long long s = want / rows;
   if (s > tiles / least) s = tiles / least;
@@ -235,7 +237,9 @@ int split_of(long long rows, int tiles, long long want, int least) {
 // The same for fp32, whose tiles take long enough that the last round of blocks counts: of all
 // splits the one with the least rounds * (tiles of a block + its start and end) + joining, in
 // tiles' times (dq of 1000 x 257 at 12 heads of 128: 192 blocks of 5 tiles on 148 SMs 131 us, 576
-// of 1 or 2 with the sum 106; dk, dv: 240 blocks of 4 as long as 120 of 8).
+// of 1 or 2 with the sum 106; dk, dv: 240 blocks of 4 as long as 120 of 8).  Forward in one part, as
+// chosen, in more: 2 x 777 x 333 at 3 heads of 64 34, 27 and 30 us, 1000 x 257 at 12 of 128
+// 97, 83 and 89, 64 x 8192 at 8 of 128 1184, 87 and 97, 2 x 1 x 512 at 12 of 128 76, 25 and 27.
 int even_split(long long rows, int tiles, int slots) {
   int best = 1;
   double least = 0;

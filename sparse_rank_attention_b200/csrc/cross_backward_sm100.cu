@@ -23,7 +23,7 @@
 // memory would need atomics.
 //
 // Measured: 32760 queries x 512 keys, 40 heads of 128, kv_len between half and all of the keys:
-// 1640 to 1770 us: statistics 141 (0.67 GB, 4.8 TB/s), dq 720 (3 products), dk and dv 737 (4
+// 1600 to 1770 us: statistics 141 (0.67 GB, 4.8 TB/s), dq 720 (3 products), dk and dv 737 (4
 // products), the sums of the parts 2 x 14.  As in the forward the chain of one tile bounds dq; in
 // dk, dv two of the four products wait for P^T and dS^T of the tile that they belong to.
 //

@@ -20,11 +20,12 @@
 // rows past Nq).  Blocks are persistent and walk (head, query pair) items head by head, so that
 // the blocks at work share K and V in L2.
 //
-// Measured: 75600 queries x 512 keys, 40 heads of 128 (0.79 TFLOP) 985 us back to back (804
-// TFLOP/s, 0.58 of the sustained library rate; the power limit holds the clock down) and 820 us in
-// a burst.  Neither the tensor pipe nor the exponentials nor L2 is full: what bounds it is one query
-// tile's chain S (about 1000 clocks), softmax (2300), P v (900) and the handovers between, of which
-// two run side by side.  Tried and slower: 64-key scores in two buffers (946 us in a burst), P
+// Measured: 75600 queries x 512 keys, 40 heads of 128 (0.79 TFLOP) 962 to 998 us back to back (795
+// to 825 TFLOP/s, 0.57 to 0.59 of the sustained library rate; the power limit holds the clock down)
+// and 820 us in a burst.  Neither the tensor pipe (44 % of its cycles) nor the issue slots (36 %) nor
+// L2 is full: what bounds it is one query tile's chain S, softmax, P v (by the clock in a copy made
+// to read it about 1000, 2300 and 900 clocks) and the handovers between, of which two run side by
+// side.  Tried and slower: 64-key scores in two buffers (946 us in a burst), P
 // through shared memory (1000), Q an item ahead with result warps of their own (1026), spinning
 // waits (1107 up), results stored from registers (1090).
 //

@@ -12,9 +12,9 @@
 // thread.  The variance is taken about the mean of the values held in registers (a second sum,
 // not E[x^2] - E[x]^2, which loses everything when the mean is large).
 //
-// Measured with x in fp32, branch and y in bf16, 5120 channels: 75600 tokens 820 to 858 us for
-// 4.64 GB (5.5 TB/s, 0.83 to 0.87 of a plain copy); the backward of 32760 tokens 530 to 570 us for
-// 3.02 GB (0.81 to 0.87).  Reads and writes mixed over five streams, as here, do not reach a copy's
+// Measured with x in fp32, branch and y in bf16, 5120 channels: 75600 tokens 820 to 870 us for
+// 4.64 GB (5.3 to 5.7 TB/s, 0.82 to 0.87 of a plain copy); the backward of 32760 tokens 530 to 580 us
+// for 3.02 GB (0.80 to 0.87).  Reads and writes mixed over five streams, as here, do not reach a copy's
 // rate.  The backward of 2331 rows of 1000 fp32 channels: 9 us and 6 for the sums of the weight.
 #include <type_traits>
 

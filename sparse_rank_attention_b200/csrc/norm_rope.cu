@@ -14,11 +14,12 @@
 // ahead, by the first threads of the group.
 //
 // Measured, bf16 with token norm and a grid: 32760 tokens x 40 heads of 128, q and k, 223 us for
-// 1.34 GB (6.0 TB/s, 0.92 of a plain copy).  The backward of 12 heads, 131 us for 0.60 GB (0.71 of
-// a copy): there the instructions set the pace, about 430 per warp and row of 512 channels at 0.6
-// of the issue slots (unpacking three bf16 operands, the rotation, two dots, two sums over the
-// group), with 15 warps an SM at 127 registers.  Small calls (2 x 1000 tokens of 2 heads) take the
-// launch's 11 us.
+// 1.34 GB (6.0 TB/s, 0.92 of a plain copy).  The backward of 12 heads, 131 to 137 us for 0.60 GB
+// (0.68 to 0.71 of a copy): there the instructions set the pace, about 430 per warp and row of 512
+// channels at 0.6 of the issue slots (unpacking three bf16 operands, the rotation, two dots, two
+// sums over the group), with 15 warps an SM at 127 registers and the block's barrier in every row.
+// The same with fp32 gradients, 198 us for 0.81 GB (0.62); of 40 heads, 533 us with bf16 gradients
+// (0.58) and 570 with fp32 (0.72).  Small calls (2 x 1000 tokens of 2 heads) take the launch's 11 us.
 #include <cmath>
 #include <type_traits>
 
