@@ -23,6 +23,9 @@ size_t elem_size(rola_dtype t) { return t == ROLA_F32 ? 4 : 2; }
 bool known(rola_dtype t) { return t == ROLA_F32 || t == ROLA_BF16 || t == ROLA_FP8_E4M3; }
 rola_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ROLA_OK : ROLA_ERR_CUDA; }
 
+// Whether so many elements lie within an address space; the spans below then fit 64 bits.
+bool reachable(double elements, size_t el) { return elements * el < (double)(1ll << 48); }
+
 // A strided [B, N, H, d] tensor; the strides of axes of size one take those of a contiguous one.
 struct View {
   const char* p;
@@ -42,7 +45,7 @@ struct View {
     const int64_t unit = (int64_t)(16 / el);
     for (int64_t x : {s.b, s.n, s.h})
       if (x < d || x % unit != 0 || x > (1ll << 36)) return false;   // 2^36: in reach of a tensor map
-    return true;
+    return reachable((double)(B - 1) * s.b + (double)(N - 1) * s.n + (double)(H - 1) * s.h + d, el);
   }
   size_t span() const { return el * (size_t)((B - 1) * s.b + (int64_t)(N - 1) * s.n + (int64_t)(H - 1) * s.h + d); }
   // no two of its elements share memory (for tensors that are written in place)
@@ -177,6 +180,7 @@ size_t mod_span(const rola_gated_norm_params& p, int64_t sb, int64_t st) {
   if (p.B == 1) sb = 0;
   if (p.T == 1) st = 0;
   if (sb < 0 || st < 0 || sb % 4 != 0 || st % 4 != 0) return 0;
+  if (!reachable((double)(p.B - 1) * sb + (double)(p.T - 1) * st + p.C, 4)) return 0;
   return 4 * (size_t)((p.B - 1) * sb + (p.T - 1) * st + p.C);
 }
 

@@ -374,3 +374,18 @@ def test_cross_of_the_most_tokens(n, code):
             for kw in (dict(Nq=n, Nk=64), dict(Nq=64, Nk=n)):
                 got, need = size(fn, cross_params(B=1, H=1, dtype=dtype, **kw))
                 assert got == code and (code or need < 2 ** 50)
+
+
+@pytest.mark.parametrize("fn,p,base,kw", [
+    ("rola_qk_norm_rope", lambda: rope_params(B=1, N=1 << 29, q=(ctypes.c_int64 * 3)(0, 1 << 35, 64)), ROPE, {}),
+    ("rola_qk_norm_rope_backward", lambda: rope_params(B=1, N=1 << 29, k=(ctypes.c_int64 * 3)(0, 1 << 35, 64)), ROPE_BACK,
+     dict(ws=at(15), n=1 << 27)),
+    ("rola_gated_norm", lambda: norm_params(gate_b=1 << 62), NORM, {}),
+    ("rola_gated_norm", lambda: norm_params(B=1, T=30, shift_t=1 << 60), NORM, {}),
+    ("rola_gated_norm_backward", lambda: norm_params(scale_b=1 << 50), NORM_BACK, dict(ws=at(15), n=1 << 27)),
+    ("rola_cross_attend", lambda: cross_params(B=1, H=1, Nk=1 << 29, v=(ctypes.c_int64 * 3)(0, 1 << 35, 64)), CROSS,
+     dict(ws=at(15), n=1 << 27)),
+])
+def test_strides_past_an_address_space(fn, p, base, kw):
+    """Whose extents would wrap in 64 bits, and with them the checks against overlaps."""
+    assert call(fn, p(), base, kw) == INVALID

@@ -21,6 +21,7 @@ def _cuda():
     rola.load()
     yield
     assert rola.block_poll_status() == 0
+    torch.cuda.empty_cache()                  # tests in other processes follow
 
 
 def _gen(seed):
