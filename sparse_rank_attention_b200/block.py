@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import numbers
 
 import torch
 
@@ -95,10 +96,12 @@ def _m(t):
 
 
 def _number(where, name, x):
+    # a tensor is none: checks are kept by their arguments, which must not change behind them
+    _need(isinstance(x, numbers.Real), where, f"{name} is not a number")
     try:
         return float(x)
-    except (TypeError, ValueError, OverflowError):
-        raise RolaError(_INVALID, f"{where}: {name} is not a number") from None
+    except OverflowError:
+        raise RolaError(_INVALID, f"{where}: {name} is not a number of a double's range") from None
 
 
 def _results(where, out, n):
@@ -229,7 +232,7 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, *, norm="token", eps=1e-6, grid=No
     where = "rola_qk_norm_rope"
     mq = _m(q)
     p = _rope(where, mq, _m(k), _m(wq), _m(wk), _m(positions), None, None, norm, eps,
-              None if grid is None else tuple(grid), tuple(start), tuple(pairs), rope_base, rope)
+              None if grid is None else tuple(grid), tuple(start), tuple(pairs), rope_base, bool(rope))
     if out is None:
         qo, ko = _new(q), None if k is None else _new(k)
     else:
@@ -262,7 +265,7 @@ def qk_norm_rope_backward(dq_out, dk_out=None, q=None, k=None, wq=None, wk=None,
     _need(mu is not None, where, "there is no dq_out")
     dtype = mu[2] if q is None else mq[2]
     p = _rope(where, mq, _m(k), _m(wq), _m(wk), _m(positions), mu, _m(dk_out), norm, eps,
-              None if grid is None else tuple(grid), tuple(start), tuple(pairs), rope_base, rope)
+              None if grid is None else tuple(grid), tuple(start), tuple(pairs), rope_base, bool(rope))
     if norm == "none":                        # only their type counts
         q = k = None
     dq, dk = _new(dq_out, dtype), None if dk_out is None else _new(dk_out, dtype)

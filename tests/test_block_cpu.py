@@ -389,3 +389,27 @@ def test_cross_of_the_most_tokens(n, code):
 def test_strides_past_an_address_space(fn, p, base, kw):
     """Whose extents would wrap in 64 bits, and with them the checks against overlaps."""
     assert call(fn, p(), base, kw) == INVALID
+
+
+@pytest.mark.parametrize("make,text", [
+    (lambda x: rola.qk_norm_rope(Q, None, W, eps=x), "eps is not a number"),
+    (lambda x: rola.qk_norm_rope(Q, None, W, rope_base=x), "rope_base is not a number"),
+    (lambda x: rola.qk_norm_rope(Q, None, W, grid=(1, 1, x)), "grid"),
+    (lambda x: rola.gated_norm(X, eps=x), "eps is not a number"),
+    (lambda x: rola.cross_attend(Q, K, K, softmax_scale=x), "softmax_scale is not a number"),
+])
+def test_tensors_are_no_numbers(make, text):
+    """Options are kept with the checks of a call; one whose value may change later is refused."""
+    with pytest.raises(rola.RolaError, match=text):
+        make(torch.tensor(2.0))
+    with pytest.raises(rola.RolaError, match="CUDA device|grid"):
+        make(2.0)
+
+
+def test_numbers_of_every_kind():
+    import numpy as np
+    from fractions import Fraction
+    for x in (1, np.float32(1e-6), np.float64(1e-6), np.int64(1), Fraction(1, 4)):
+        assert block._number("call", "eps", x) == float(x)
+    with pytest.raises(rola.RolaError):
+        block._number("call", "eps", 10 ** 400)
